@@ -8,7 +8,9 @@ Scratch workspaces are torch allocations unless the caller passes one.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import dataclasses
 import math
 import os
 import threading
@@ -19,7 +21,9 @@ __all__ = ["CsaError", "lib", "csa_compress", "csa_compress_step", "csa_norm_rop
            "csa_index_score", "csa_index_score_q", "csa_topk_select",
            "csa_index_topk_workspace", "csa_index_topk_launches", "csa_sparse_attn", "csa_sparse_attn_workspace", "hca_attn",
            "csa_sparse_attn_ex", "hca_attn_ex", "csa_index_topk_grouped",
-           "hca_attn_workspace", "csa_grouped_out_proj", "csa_get_device_error", "csa_set_batch_invariant", "csa_set_index_fusion", "LIB_PATH", "DEVERR_NONE", "DEVERR_TIMEOUT",
+           "hca_attn_workspace", "csa_grouped_out_proj", "Fp4Matrix", "csa_fp4_scale_bytes", "csa_fp4_quantize",
+           "csa_fp4_dequantize", "csa_fp4_pack_scales", "csa_fp4_linear", "csa_grouped_out_proj_fp4",
+           "csa_grouped_out_proj_fp4_workspace", "csa_get_device_error", "csa_set_batch_invariant", "csa_set_index_fusion", "LIB_PATH", "DEVERR_NONE", "DEVERR_TIMEOUT",
            "DEVERR_INDEX"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcsa.so")
@@ -54,6 +58,10 @@ class _PoolCfg(ctypes.Structure):
                 ("in_dtype", ctypes.c_int)]
 
 
+class _Fp4Mat(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p)]
+
+
 def lib() -> ctypes.CDLL:
     """Load libcsa.so (built in-tree by ``__graft_entry__.build()``); raise if it is absent."""
     global _lib
@@ -85,6 +93,16 @@ def lib() -> ctypes.CDLL:
             L.hca_attn_workspace.argtypes = [I, I, I, I, I]
             L.hca_attn_workspace.restype = SZ
             L.csa_grouped_out_proj.argtypes = [I, I, I, I, I, I, P, P, P, P, P, P]
+            MAT = ctypes.POINTER(_Fp4Mat)
+            L.csa_fp4_scale_bytes.argtypes = [I, I64, I]
+            L.csa_fp4_scale_bytes.restype = SZ
+            L.csa_fp4_quantize.argtypes = [I, P, I, I64, I, I64, MAT, P]
+            L.csa_fp4_dequantize.argtypes = [I, MAT, I64, I, I, P, I64, P]
+            L.csa_fp4_pack_scales.argtypes = [I, P, I64, I, P, P]
+            L.csa_fp4_linear.argtypes = [I, I, I, I, I, MAT, MAT, I, P, I64, P]
+            L.csa_grouped_out_proj_fp4_workspace.argtypes = [I, I, I, I, I, I]
+            L.csa_grouped_out_proj_fp4_workspace.restype = SZ
+            L.csa_grouped_out_proj_fp4.argtypes = [I, I, I, I, I, I, I, P, P, MAT, P, MAT, P, P, SZ, P]
             L.csa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), P]
             L.csa_set_index_fusion.argtypes = [I]
             L.csa_set_index_fusion.restype = I
@@ -98,7 +116,8 @@ def lib() -> ctypes.CDLL:
                        "csa_index_score_q",
                        "csa_topk_select", "csa_sparse_attn",
                        "hca_attn", "csa_sparse_attn_ex", "hca_attn_ex", "csa_grouped_out_proj", "csa_index_topk_grouped",
-                       "csa_get_device_error"):
+                       "csa_fp4_quantize", "csa_fp4_dequantize", "csa_fp4_pack_scales", "csa_fp4_linear",
+                       "csa_grouped_out_proj_fp4", "csa_get_device_error"):
                 getattr(L, fn).restype = I
             _lib = L
     return _lib
@@ -386,6 +405,198 @@ def csa_grouped_out_proj(o, A, Bm, *, z=None, y=None):
     st = lib().csa_grouped_out_proj(T, H, D, G, R, d_model, _ptr(o), _ptr(A), _ptr(Bm), _ptr(z), _ptr(y), _stream(o))
     _check("csa_grouped_out_proj", st)
     return z, y
+
+
+_FP4_FMT = {"mxfp4": 0, "nvfp4": 1}
+_FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+
+
+@dataclasses.dataclass(frozen=True)
+class Fp4Matrix:
+    """A microscaled 4-bit matrix [rows, cols]: packed uint8 [rows, cols/2], scales uint8 in the
+    blocked layout (csa_fp4_scale_bytes bytes) and, for "nvfp4", tensor_scale float32 [1]."""
+    fmt: str
+    rows: int
+    cols: int
+    packed: torch.Tensor
+    scales: torch.Tensor
+    tensor_scale: torch.Tensor | None = None
+
+
+def _fmt(fmt: str) -> int:
+    if fmt not in _FP4_FMT:
+        raise ValueError(f'fmt must be "mxfp4" or "nvfp4", got {fmt!r}')
+    return _FP4_FMT[fmt]
+
+
+def _tensor_scale(fmt: str, g: torch.Tensor | None, dev, name="tensor_scale"):
+    if (g is not None) != (fmt == "nvfp4"):
+        raise ValueError(f"{name} goes with nvfp4, and only with it")
+    if g is None:
+        return None
+    _need(g, torch.float32, None, name)
+    if g.numel() != 1 or g.device != dev:
+        raise ValueError(f"{name} must be one value on {dev}")
+    return _ptr(g)
+
+
+def _fp4_mat(m: Fp4Matrix, name: str, dev) -> _Fp4Mat:
+    f = _fmt(m.fmt)
+    if m.rows < 0 or m.cols < 32 or m.cols % 32:
+        raise ValueError(f"{name}: cols must be a positive multiple of 32, got {m.cols}")
+    for t, nm in ((m.packed, "packed"), (m.scales, "scales")):
+        _need(t, torch.uint8, None, f"{name}.{nm}")
+        if t.device != dev:
+            raise ValueError(f"{name}.{nm} must be on {dev}, got {t.device}")
+    if m.packed.numel() != m.rows * (m.cols // 2):
+        raise ValueError(f"{name}.packed must hold {m.rows} x {m.cols // 2} bytes, got {m.packed.numel()}")
+    if m.scales.numel() < lib().csa_fp4_scale_bytes(f, m.rows, m.cols):
+        raise ValueError(f"{name}.scales is smaller than csa_fp4_scale_bytes({m.fmt}, {m.rows}, {m.cols})")
+    return _Fp4Mat(_ptr(m.packed), _ptr(m.scales), _tensor_scale(m.fmt, m.tensor_scale, dev, f"{name}.tensor_scale"))
+
+
+def _rows_2d(t: torch.Tensor, name: str):
+    """[..., cols] as evenly spaced rows: (rows, cols, elements between rows)."""
+    if t.dim() < 1 or (t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have contiguous rows")
+    cols = t.shape[-1]
+    rows = t.numel() // cols if cols else 0
+    if t.dim() == 1 or rows <= 1:
+        return rows, cols, cols
+    ld = t.stride(-2) if t.shape[-2] > 1 else 0
+    for i in range(t.dim() - 3, -1, -1):  # every outer dimension must continue the same spacing
+        if t.shape[i] > 1:
+            inner = math.prod(t.shape[i + 1:-1])
+            if ld == 0:
+                if t.stride(i) % inner:
+                    raise ValueError(f"{name}'s rows are not evenly spaced")
+                ld = t.stride(i) // inner
+            if t.stride(i) != ld * inner:
+                raise ValueError(f"{name}'s rows are not evenly spaced")
+    return rows, cols, ld
+
+
+def _on(t: torch.Tensor):
+    """The device guard of a call on t's device (nothing when it is the current one)."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def csa_fp4_scale_bytes(fmt: str, rows: int, cols: int) -> int:
+    return int(lib().csa_fp4_scale_bytes(_fmt(fmt), rows, cols))
+
+
+def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch.Tensor | None = None,
+                     out: Fp4Matrix | None = None) -> Fp4Matrix:
+    """x [..., cols] float32/bf16 (evenly spaced rows, cols a multiple of 32) -> Fp4Matrix [rows, cols].
+    nvfp4 takes the tensor's scale (float32 [1], e.g. amax / 2688); `out` reuses a matrix's buffers."""
+    f, dt, dev = _fmt(fmt), _dt(x), x.device
+    rows, cols, ld = _rows_2d(x, "x")
+    if cols < 32 or cols % 32:
+        raise ValueError(f"x's last dimension must be a positive multiple of 32, got {cols}")
+    if out is None:
+        out = Fp4Matrix(fmt, rows, cols, torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
+                        torch.empty(lib().csa_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8, device=dev),
+                        tensor_scale)
+    elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
+        raise ValueError(f"out must be a {fmt} matrix of {rows} x {cols}")
+    elif out.tensor_scale is not tensor_scale:
+        out = dataclasses.replace(out, tensor_scale=tensor_scale)
+    with _on(x):
+        m = _fp4_mat(out, "out", dev)
+        st = lib().csa_fp4_quantize(f, ctypes.c_void_p(x.data_ptr()), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
+    _check("csa_fp4_quantize", st)
+    return out
+
+
+def csa_fp4_dequantize(m: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None):
+    """The values of m, [rows, cols] in dtype (float32 or bf16), or into `out` (evenly spaced rows)."""
+    dev = m.packed.device
+    if out is None:
+        out = torch.empty((m.rows, m.cols), dtype=dtype, device=dev)
+    rows, cols, ld = _rows_2d(out, "out")
+    if (rows, cols) != (m.rows, m.cols) or out.device != dev:
+        raise ValueError(f"out must be {m.rows} x {m.cols} on {dev}")
+    with _on(m.packed):
+        c = _fp4_mat(m, "m", dev)
+        st = lib().csa_fp4_dequantize(_fmt(m.fmt), ctypes.byref(c), rows, cols, _dt(out), ctypes.c_void_p(out.data_ptr()),
+                                      ld, _stream(out))
+    _check("csa_fp4_dequantize", st)
+    return out
+
+
+def csa_fp4_pack_scales(scales: torch.Tensor, cols: int, *, fmt: str = "mxfp4") -> torch.Tensor:
+    """Row-major scale bytes uint8 [rows, cols / block] (csa_quantize_mxfp4's) -> the blocked layout."""
+    f = _fmt(fmt)
+    _need(scales, torch.uint8, None, "scales")
+    if cols < 32 or cols % 32 or scales.dim() < 2 or scales.shape[-1] != cols // _FP4_BLOCK[fmt]:
+        raise ValueError(f"scales must have {cols} / {_FP4_BLOCK[fmt]} bytes a row, got {tuple(scales.shape)}")
+    rows = scales.numel() // scales.shape[-1]
+    out = torch.empty(lib().csa_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8, device=scales.device)
+    with _on(scales):
+        st = lib().csa_fp4_pack_scales(f, _ptr(scales), rows, cols, _ptr(out), _stream(scales))
+    _check("csa_fp4_pack_scales", st)
+    return out
+
+
+def csa_fp4_linear(x: Fp4Matrix, w: Fp4Matrix, *, groups: int = 1, out_dtype: torch.dtype = torch.bfloat16,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """x [M, G K] times w [G N, K] group by group -> y [M, G N] (bf16 or float32)."""
+    dev = x.packed.device
+    if x.fmt != w.fmt:
+        raise ValueError(f"x is {x.fmt} and w is {w.fmt}")
+    G, M, K = groups, x.rows, w.cols
+    if G < 1 or w.rows % G or x.cols != G * K:
+        raise ValueError(f"x {x.rows} x {x.cols} and w {w.rows} x {w.cols} do not fit {G} groups")
+    N = w.rows // G
+    if out is None:
+        out = torch.empty((M, G * N), dtype=out_dtype, device=dev)
+    dt = _dt(out)
+    rows, cols, ld = _rows_2d(out, "out")
+    if (rows, cols) != (M, G * N) or out.device != dev:
+        raise ValueError(f"out must be {M} x {G * N} on {dev}")
+    with _on(x.packed):
+        cx, cw = _fp4_mat(x, "x", dev), _fp4_mat(w, "w", dev)
+        st = lib().csa_fp4_linear(_fmt(x.fmt), M, N, K, G, ctypes.byref(cx), ctypes.byref(cw), dt,
+                                  ctypes.c_void_p(out.data_ptr()), ld, _stream(x.packed))
+    _check("csa_fp4_linear", st)
+    return out
+
+
+def csa_grouped_out_proj_fp4_workspace(fmt: str, T: int, H: int, D: int, G: int, R: int) -> int:
+    return int(lib().csa_grouped_out_proj_fp4_workspace(_fmt(fmt), T, H, D, G, R))
+
+
+def csa_grouped_out_proj_fp4(o: torch.Tensor, A: Fp4Matrix, Bm: Fp4Matrix, *, groups: int,
+                             o_scale: torch.Tensor | None = None, z_scale: torch.Tensor | None = None,
+                             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Grouped output projection on FP4 weights: o [T, H, D] bf16; A [G R, (H/G) D]; Bm [d_model, G R].
+    nvfp4 takes the calibrated tensor scales of o and of the intermediate z.  Returns y [T, d_model] bf16."""
+    T, H, D = o.shape
+    dev, fmt, G = o.device, A.fmt, groups
+    _need(o, torch.bfloat16, None, "o")
+    if A.fmt != Bm.fmt:
+        raise ValueError(f"A is {A.fmt} and Bm is {Bm.fmt}")
+    if G < 1 or H % G or A.rows % G or A.cols * G != H * D or Bm.cols != A.rows:
+        raise ValueError("inconsistent projection shapes")
+    R, d_model = A.rows // G, Bm.rows
+    need = csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R)
+    if out is None:
+        out = torch.empty((T, d_model), dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, (T, d_model), "out")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out.device != dev or workspace.device != dev:
+        raise ValueError(f"out and workspace must be on {dev}")
+    with _on(o):
+        ca, cb = _fp4_mat(A, "A", dev), _fp4_mat(Bm, "Bm", dev)
+        st = lib().csa_grouped_out_proj_fp4(_fmt(fmt), T, H, D, G, R, d_model, _ptr(o),
+                                            _tensor_scale(fmt, o_scale, dev, "o_scale"), ctypes.byref(ca),
+                                            _tensor_scale(fmt, z_scale, dev, "z_scale"), ctypes.byref(cb), _ptr(out),
+                                            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(o))
+    _check("csa_grouped_out_proj_fp4", st)
+    return out
 
 
 def csa_set_index_fusion(on: bool) -> None:

@@ -502,6 +502,141 @@ csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d_model, 
   return from_cuda(launch_grouped_out_proj(a, stream));
 }
 
+// ------------------------------------------------------------------ microscaled 4-bit matrices
+static bool fp4_format_ok(csa_fp4_format f) { return f == CSA_MXFP4 || f == CSA_NVFP4; }
+
+// A matrix argument of rows x cols: pointers present and aligned, a tensor scale with NVFP4 only.
+static csa_status fp4_mat_status(csa_fp4_format f, const csa_fp4_mat* m) {
+  if (m == nullptr || m->packed == nullptr || m->scales == nullptr) return CSA_ERR_INVALID_ARG;
+  if ((m->tensor_scale != nullptr) != (f == CSA_NVFP4)) return CSA_ERR_INVALID_ARG;
+  if (!aligned16(m->packed) || !aligned16(m->scales) || (reinterpret_cast<uintptr_t>(m->tensor_scale) & 3u) != 0)
+    return CSA_ERR_ALIGNMENT;
+  return CSA_OK;
+}
+
+size_t csa_fp4_scale_bytes(csa_fp4_format fmt, int64_t rows, int cols) {
+  if (!fp4_format_ok(fmt) || rows < 0 || cols < 1) return 0;
+  return fp4_scale_bytes(fmt == CSA_NVFP4, rows, cols);
+}
+
+csa_status csa_fp4_quantize(csa_fp4_format fmt, const void* x, csa_dtype dtype, int64_t rows, int cols, int64_t ld,
+                            const csa_fp4_mat* out, cudaStream_t stream) {
+  if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0 || ld < cols) return CSA_ERR_INVALID_ARG;
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (rows == 0) return CSA_OK;
+  if (x == nullptr) return CSA_ERR_INVALID_ARG;
+  const csa_status st = fp4_mat_status(fmt, out);
+  if (st != CSA_OK) return st;
+  if (!aligned16(x) || ld % (dtype == CSA_BF16 ? 8 : 4) != 0) return CSA_ERR_ALIGNMENT;
+  return from_cuda(launch_fp4_quantize(fmt == CSA_NVFP4, x, dtype == CSA_BF16, rows, cols, ld, out->tensor_scale,
+                                       const_cast<uint8_t*>(out->packed), const_cast<uint8_t*>(out->scales), stream));
+}
+
+csa_status csa_fp4_dequantize(csa_fp4_format fmt, const csa_fp4_mat* m, int64_t rows, int cols, csa_dtype dtype,
+                              void* out, int64_t ld, cudaStream_t stream) {
+  if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0 || ld < cols) return CSA_ERR_INVALID_ARG;
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
+  if (rows == 0) return CSA_OK;
+  if (out == nullptr) return CSA_ERR_INVALID_ARG;
+  const csa_status st = fp4_mat_status(fmt, m);
+  if (st != CSA_OK) return st;
+  if (!aligned16(out) || ld % (dtype == CSA_BF16 ? 8 : 4) != 0) return CSA_ERR_ALIGNMENT;
+  return from_cuda(launch_fp4_dequantize(fmt == CSA_NVFP4, m->packed, m->scales, m->tensor_scale, rows, cols,
+                                         dtype == CSA_BF16, out, ld, stream));
+}
+
+csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales, int64_t rows, int cols, uint8_t* out,
+                               cudaStream_t stream) {
+  if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0) return CSA_ERR_INVALID_ARG;
+  if (rows == 0) return CSA_OK;
+  if (scales == nullptr || out == nullptr) return CSA_ERR_INVALID_ARG;
+  if (!aligned16(out)) return CSA_ERR_ALIGNMENT;
+  return from_cuda(launch_fp4_pack_scales(fmt == CSA_NVFP4, scales, rows, cols, out, stream));
+}
+
+// Sizes of a product: K a multiple of 32; groups split at whole scale blocks (128 rows of W,
+// 128 columns); byte counts and row counts within TMA's 32-bit coordinates.
+static csa_status fp4_product_status(int64_t M, int64_t N, int64_t K, int64_t G) {
+  if (M < 0 || N < 1 || K < 1 || G < 1) return CSA_ERR_INVALID_ARG;
+  if (K % 32 != 0 || (G > 1 && (K % 128 != 0 || N % 128 != 0))) return CSA_ERR_UNSUPPORTED;
+  if (G * K > 0x7fffffffLL || G * N > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
+  return CSA_OK;
+}
+
+csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x, const csa_fp4_mat* w,
+                          csa_dtype y_dtype, void* y, int64_t ldy, cudaStream_t stream) {
+  if (!fp4_format_ok(fmt) || (y_dtype != CSA_F32 && y_dtype != CSA_BF16)) return CSA_ERR_INVALID_ARG;
+  csa_status st = fp4_product_status(M, N, K, G);
+  if (st != CSA_OK) return st;
+  if (ldy < static_cast<int64_t>(G) * N) return CSA_ERR_INVALID_ARG;
+  if (M == 0) return CSA_OK;
+  if ((st = fp4_mat_status(fmt, x)) != CSA_OK || (st = fp4_mat_status(fmt, w)) != CSA_OK) return st;
+  if (y == nullptr) return CSA_ERR_INVALID_ARG;
+  if (!aligned16(y)) return CSA_ERR_ALIGNMENT;
+  Fp4LinearArgs a{};
+  a.nv = fmt == CSA_NVFP4;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.G = G;
+  a.x_packed = x->packed;
+  a.x_scale = x->scales;
+  a.gx = x->tensor_scale;
+  a.w_packed = w->packed;
+  a.w_scale = w->scales;
+  a.gw = w->tensor_scale;
+  a.out_bf16 = y_dtype == CSA_BF16;
+  a.y = y;
+  a.ldy = ldy;
+  return from_cuda(launch_fp4_linear(a, stream));
+}
+
+size_t csa_grouped_out_proj_fp4_workspace(csa_fp4_format fmt, int T, int H, int D, int G, int R) {
+  if (!fp4_format_ok(fmt) || T < 0 || H < 1 || D < 1 || G < 1 || R < 1) return 0;
+  const int64_t HD = static_cast<int64_t>(H) * D, GR = static_cast<int64_t>(G) * R;
+  if (HD > 0x7fffffffLL || GR > 0x7fffffffLL) return 0;
+  return fp4_proj_workspace_bytes(fmt == CSA_NVFP4, T, HD, GR);
+}
+
+csa_status csa_grouped_out_proj_fp4(csa_fp4_format fmt, int T, int H, int D, int G, int R, int d_model, const void* o,
+                                    const float* o_scale, const csa_fp4_mat* A, const float* z_scale,
+                                    const csa_fp4_mat* Bm, void* y, void* workspace, size_t ws_bytes,
+                                    cudaStream_t stream) {
+  if (!fp4_format_ok(fmt) || T < 0 || H < 1 || D < 1 || G < 1 || R < 1 || d_model < 1 || H % G != 0)
+    return CSA_ERR_INVALID_ARG;
+  const int64_t Kg = static_cast<int64_t>(H / G) * D;
+  if (Kg % 128 != 0 || R % 128 != 0) return CSA_ERR_UNSUPPORTED;
+  csa_status st = fp4_product_status(T, R, Kg, G);
+  if (st == CSA_OK) st = fp4_product_status(T, d_model, static_cast<int64_t>(G) * R, 1);
+  if (st != CSA_OK) return st;
+  if (T == 0) return CSA_OK;
+  if (!o || !y || !workspace) return CSA_ERR_INVALID_ARG;
+  if ((st = fp4_mat_status(fmt, A)) != CSA_OK || (st = fp4_mat_status(fmt, Bm)) != CSA_OK) return st;
+  if ((o_scale != nullptr) != (fmt == CSA_NVFP4) || (z_scale != nullptr) != (fmt == CSA_NVFP4))
+    return CSA_ERR_INVALID_ARG;
+  if (!aligned16(o) || !aligned16(y) || !aligned16(workspace)) return CSA_ERR_ALIGNMENT;
+  if (ws_bytes < csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R)) return CSA_ERR_WORKSPACE;
+  Fp4ProjArgs a{};
+  a.nv = fmt == CSA_NVFP4;
+  a.T = T;
+  a.G = G;
+  a.Kg = static_cast<int>(Kg);
+  a.R = R;
+  a.d_model = d_model;
+  a.o = o;
+  a.go = o_scale;
+  a.gz = z_scale;
+  a.a_packed = A->packed;
+  a.a_scale = A->scales;
+  a.ga = A->tensor_scale;
+  a.b_packed = Bm->packed;
+  a.b_scale = Bm->scales;
+  a.gb = Bm->tensor_scale;
+  a.y = y;
+  a.ws = workspace;
+  return from_cuda(launch_grouped_out_proj_fp4(a, stream));
+}
+
 csa_status csa_get_device_error(int32_t* code_out, cudaStream_t stream) {
   if (code_out == nullptr) return CSA_ERR_INVALID_ARG;
   int32_t* d = device_error_word();

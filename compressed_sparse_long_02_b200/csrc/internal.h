@@ -112,6 +112,48 @@ cudaError_t launch_pool(const PoolArgs& a, cudaStream_t s);
 cudaError_t launch_quantize_mxfp4(const void* x, int in_bf16, int64_t rows, int cols, uint8_t* packed,
                                   uint8_t* scales, cudaStream_t s);
 
+// ---------------------------------------------------------------- microscaled 4-bit matrices
+// (nv: NVFP4, else MXFP4; see fp4.cu for the scale layout)
+size_t fp4_scale_bytes(bool nv, int64_t rows, int cols);
+cudaError_t launch_fp4_quantize(bool nv, const void* x, int in_bf16, int64_t rows, int cols, int64_t ld,
+                                const float* tensor_scale, uint8_t* packed, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(bool nv, const uint8_t* packed, const uint8_t* scales, const float* tensor_scale,
+                                  int64_t rows, int cols, int out_bf16, void* out, int64_t ld, cudaStream_t s);
+cudaError_t launch_fp4_pack_scales(bool nv, const uint8_t* in, int64_t rows, int cols, uint8_t* out, cudaStream_t s);
+
+struct Fp4LinearArgs {
+  bool nv;
+  int M, N, K, G;
+  const uint8_t* x_packed;  // [M, G K / 2]
+  const uint8_t* x_scale;
+  const float* gx;          // tensor scales (NVFP4; nullable = 1)
+  const uint8_t* w_packed;  // [G N, K / 2]
+  const uint8_t* w_scale;
+  const float* gw;
+  int out_bf16;
+  void* y;                  // [M, ldy]
+  int64_t ldy;
+};
+cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s);
+
+struct Fp4ProjArgs {
+  bool nv;
+  int T, G, Kg, R, d_model;  // Kg = (H / G) D
+  const void* o;             // bf16 [T, G Kg]
+  const float* go;           // tensor scales of o and z (NVFP4)
+  const float* gz;
+  const uint8_t* a_packed;   // [G R, Kg / 2]
+  const uint8_t* a_scale;
+  const float* ga;
+  const uint8_t* b_packed;   // [d_model, G R / 2]
+  const uint8_t* b_scale;
+  const float* gb;
+  void* y;                   // bf16 [T, d_model]
+  void* ws;
+};
+size_t fp4_proj_workspace_bytes(bool nv, int T, int64_t HD, int64_t GR);
+cudaError_t launch_grouped_out_proj_fp4(const Fp4ProjArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- indexer + top-k
 struct IndexArgs {
   int Nq, Hi, Di, k, m, B, E_max;

@@ -18,6 +18,9 @@
  *   hca_attn            shared-KV MQA over every visible HCA entry plus the window.
  *   csa_sparse_attn_ex, hca_attn_ex  the same with the query's RMSNorm + RoPE applied in the kernel.
  *   csa_grouped_out_proj  grouped projection of the head outputs to the hidden size.
+ *   csa_fp4_quantize, csa_fp4_dequantize, csa_fp4_linear, csa_grouped_out_proj_fp4
+ *                       microscaled 4-bit matrices (MXFP4, NVFP4), their product, and the grouped
+ *                       projection on FP4 weights.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers unless marked "host".  The caller
@@ -369,6 +372,77 @@ CSA_API csa_status hca_attn_ex(const csa_q_prep* prep, int Nq, int H, int D, int
  */
 CSA_API csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d_model, const void* o, const void* A,
                                         const void* Bm, void* z, void* y, cudaStream_t stream);
+
+/*
+ * Microscaled 4-bit matrices (the pages run the model's weights and the indexer in FP4; dev.to
+ * "How DeepSeek-V4 Achieves ...").  A matrix [rows, cols], cols a multiple of 32, is
+ *   packed        uint8 [rows, cols/2]: E2M1 codes, element 2i in the low nibble of byte i;
+ *   scales        uint8, one per block of a row's consecutive elements, in the layout below;
+ *   tensor_scale  device float32, one value g > 0 (NVFP4), or NULL (MXFP4: g = 1).
+ *
+ * CSA_MXFP4: blocks of 32, the codes and UE8M0 scales of csa_quantize_mxfp4; value = code * 2^E.
+ * CSA_NVFP4: blocks of 16, E4M3 scales; value = code * s * g.  Encoding, every step rounded once
+ *   to float32: s = e4m3(amax / (6 g)) (to nearest even, at most 448), T = s g,
+ *   code = e2m1(x / T) (to nearest even, at most 6; 0 when T = 0).
+ * In both a NaN is left out of amax and encoded as +6, and an infinity counts as 2^128 in amax
+ * (E = 126; s = 448) and is encoded as +-6.
+ *
+ * Scale layout: rows in blocks of 128, a row's scales in atoms of 4; atom (row block i, atom a) is
+ * the 512 bytes at ((i * n_atoms) + a) * 512, n_atoms = ceil(cols / (4 * block)), and its scale
+ * (r, b), r < 128, b < 4, is byte (r % 32) * 16 + (r / 32) * 4 + b.  Rows and scales that only pad
+ * an atom are stored as 0.  csa_fp4_scale_bytes gives the size (0 for invalid arguments).
+ */
+typedef enum { CSA_MXFP4 = 0, CSA_NVFP4 = 1 } csa_fp4_format;
+
+typedef struct {
+  const uint8_t* packed;
+  const uint8_t* scales;
+  const float* tensor_scale; /* device; NVFP4: required, MXFP4: NULL */
+} csa_fp4_mat;
+
+CSA_API size_t csa_fp4_scale_bytes(csa_fp4_format fmt, int64_t rows, int cols);
+
+/*
+ * csa_fp4_quantize -- encodes x [rows, cols] (dtype; rows `ld` elements apart, ld a multiple of 8
+ * for bf16 and of 4 for float32) into the buffers of `out`, padding scales included.  out's
+ * tensor_scale is read, not computed.  Bit-exact: a pure function of the input bits.
+ * csa_fp4_dequantize -- the values of a matrix, float32 or rounded once to bf16, rows `ld` apart.
+ *   A scale byte of 255 (MXFP4) or 127 (NVFP4) reads as NaN; values past float32 are infinite.
+ * csa_fp4_pack_scales -- row-major scale bytes [rows, cols / block] (csa_quantize_mxfp4's, or a
+ *   checkpoint's) into the layout above; weights need it once.
+ */
+CSA_API csa_status csa_fp4_quantize(csa_fp4_format fmt, const void* x, csa_dtype dtype, int64_t rows, int cols,
+                                    int64_t ld, const csa_fp4_mat* out, cudaStream_t stream);
+CSA_API csa_status csa_fp4_dequantize(csa_fp4_format fmt, const csa_fp4_mat* m, int64_t rows, int cols,
+                                      csa_dtype dtype, void* out, int64_t ld, cudaStream_t stream);
+CSA_API csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales, int64_t rows, int cols,
+                                       uint8_t* out, cudaStream_t stream);
+
+/*
+ * csa_fp4_linear -- product of two matrices of one format:
+ *   y[m, g N + n] = gx gw sum_k X[m, g K + k] W[g N + n, k],   g < G, n < N, k < K
+ * x: [M, G K]; w: [G N, K]; y: [M, ldy] in y_dtype, ldy >= G N (columns past G N are left as they
+ * are).  One call for every M, from a decode token to a prefill.  float32 accumulation, one
+ * rounding to y_dtype; the result does not depend on timing, but it may differ between values of
+ * M (the K axis is split over CTAs when there are few tiles).
+ * Supported: K a multiple of 32; with G > 1, K and N multiples of 128.  No workspace.
+ */
+CSA_API csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x,
+                                  const csa_fp4_mat* w, csa_dtype y_dtype, void* y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * csa_grouped_out_proj_fp4 -- csa_grouped_out_proj with FP4 weights A [G R, (H/G) D] and
+ * Bm [d_model, G R]: o (bf16 [T, H, D]) is encoded with o_scale, each group multiplied by its own
+ * matrix, z rounded to bf16 and encoded with z_scale, then multiplied by Bm; y bf16 [T, d_model].
+ * o_scale, z_scale: device float32 tensor scales (NVFP4; calibrated by the caller), NULL for MXFP4.
+ * workspace: csa_grouped_out_proj_fp4_workspace bytes (0 for invalid arguments).
+ * Supported: (H/G) D and R multiples of 128.
+ */
+CSA_API size_t csa_grouped_out_proj_fp4_workspace(csa_fp4_format fmt, int T, int H, int D, int G, int R);
+CSA_API csa_status csa_grouped_out_proj_fp4(csa_fp4_format fmt, int T, int H, int D, int G, int R, int d_model,
+                                            const void* o, const float* o_scale, const csa_fp4_mat* A,
+                                            const float* z_scale, const csa_fp4_mat* Bm, void* y, void* workspace,
+                                            size_t ws_bytes, cudaStream_t stream);
 
 /* Synchronises `stream`, returns the device error word of the current device in
  * *code_out and clears it.  CSA_ERR_CUDA if the stream reports an error. */

@@ -1,0 +1,299 @@
+"""Microscaled 4-bit matrices on the GPU against a plain 64-bit reference.
+
+Encoding and the scale layout must match byte for byte; decoding is exact in float32 for
+values with few bits and one rounding otherwise.  A product's terms are exact (4-bit codes,
+scales of at most 4 significant bits), so the error left is float32 accumulation -- one
+addition of a K = 64 step's sum per step, each within 2^-23 of the running sums, all bounded by
+sum |x w| -- plus the rounding of the result (half a step: 2^-8 relative in bf16, 2^-24 in
+float32) and three float32 products with the tensor scales.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import fp4_reference as R
+from tests.helpers import t2np
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ["mxfp4", "nvfp4"]
+
+
+@pytest.fixture(scope="module")
+def B(cuda):
+    from compressed_sparse_long_02_b200 import binding
+    binding.lib()
+    return binding
+
+
+def tensor_scale(x, dev):
+    return torch.tensor([np.abs(x[np.isfinite(x)]).max() / 2688.0], dtype=torch.float32, device=dev)
+
+
+def make(B, dev, rng, rows, cols, fmt, std=1.0):
+    """A matrix encoded by the reference, on the device, and its float64 values."""
+    x = (rng.standard_normal((rows, cols)) * std * 2.0 ** rng.integers(-3, 4, (1, cols))).astype(np.float32)
+    x[rng.random((rows, cols)) < 0.02] = 0.0
+    g = np.float32(np.abs(x).max() / 2688.0) if fmt == "nvfp4" else None
+    codes, sb = R.encode(x, fmt, g)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    m = B.Fp4Matrix(fmt, rows, cols, up(R.pack(codes)), up(R.block_scales(sb)),
+                    None if g is None else torch.tensor([g], device=dev))
+    return m, R.decode(codes, sb, fmt, g)
+
+
+def product(x, w, G):
+    """(sum x w, sum |x w|) in float64."""
+    parts = [(a @ b.T, np.abs(a) @ np.abs(b).T) for a, b in zip(np.split(x, G, 1), np.split(w, G, 0))]
+    return np.concatenate([p[0] for p in parts], 1), np.concatenate([p[1] for p in parts], 1)
+
+
+def assert_product(y, ref, mag, K, dtype, what=""):
+    steps = -(-K // 64) + 8  # the additions of the K steps, and of up to eight split partials
+    tol = (steps * 2.0 ** -23 + 4 * 2.0 ** -24) * mag + torch.finfo(dtype).eps / 2 * np.abs(ref)
+    y = y.double().cpu().numpy()
+    assert np.isfinite(y).all(), what
+    bad = np.abs(y - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} off, worst {np.max(np.abs(y - ref) / np.maximum(tol, 1e-300)):.2f} x the bound"
+
+
+QUANT_SHAPES = [(1, 32), (1, 32768), (5, 64), (31, 96), (128, 128), (129, 160), (300, 4128), (64, 256)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", QUANT_SHAPES)
+def test_encode_matches_reference(B, cuda, fmt, dtype, rows, cols):
+    rng = np.random.default_rng(rows * 7 + cols)
+    x = torch.from_numpy((rng.standard_normal((rows, cols)) * 2.0 ** rng.integers(-9, 9, (rows, 1))).astype(np.float32))
+    x[rows // 2, : cols // 2] = 0.0  # whole zero blocks
+    x = x.to(dtype).to(cuda)
+    xf = x.float().cpu().numpy()
+    g = tensor_scale(xf, cuda) if fmt == "nvfp4" else None
+    m = B.csa_fp4_quantize(x, fmt=fmt, tensor_scale=g)
+    codes, sb = R.encode(xf, fmt, None if g is None else g.item())
+    assert np.array_equal(t2np(m.scales), R.block_scales(sb))
+    assert np.array_equal(R.unpack(t2np(m.packed)), codes)
+    # decode: exact in float32 where the value has few bits, else one rounding of code * fl(s g)
+    v32 = t2np(B.csa_fp4_dequantize(m, dtype=torch.float32)).astype(np.float64)
+    ref = R.decode(codes, sb, fmt, None if g is None else g.item())
+    assert (np.abs(v32 - ref) <= (0.0 if fmt == "mxfp4" else 2 * 2.0 ** -24) * np.abs(ref)).all()
+    assert torch.equal(B.csa_fp4_dequantize(m), torch.from_numpy(v32).float().to(torch.bfloat16).to(cuda))
+    assert B.csa_get_device_error() == 0
+
+
+def test_encode_agrees_with_quantize_mxfp4_and_pack_scales(B, cuda):
+    x = torch.randn((77, 416), device=cuda)
+    packed, scales = B.csa_quantize_mxfp4(x)
+    m = B.csa_fp4_quantize(x)
+    assert torch.equal(m.packed, packed)
+    assert torch.equal(m.scales, B.csa_fp4_pack_scales(scales, 416))
+    assert np.array_equal(t2np(m.scales), R.block_scales(t2np(scales)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_encode_borders_and_special_values(B, cuda, fmt):
+    """Every E2M1 rounding border and its float32 neighbours under exact scales, signed zeros,
+    subnormals, NaN (left out of amax, +6) and infinities."""
+    edges = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 0.0, 4.0], np.float32)
+    vals = np.concatenate([edges, np.nextafter(edges, np.float32(9)), np.nextafter(edges, np.float32(-9))])
+    vals = np.concatenate([vals, -vals])
+    rows = []
+    for k in range(0, len(vals), 15):  # each block of 16 holds a 6, so the scale is 2^0 (and s = 1 / g exactly)
+        c = vals[k:k + 15]
+        rows.append(np.concatenate([[6.0], c, np.zeros(15 - len(c))]))
+    x = np.stack([np.concatenate([r, r]) for r in rows]).astype(np.float32)
+    special = np.zeros((5, 32), np.float32)
+    special[0, :4] = [np.nan, 1.0, -2.0, -np.nan]
+    special[1, :3] = [np.inf, 1.0, -3.0]
+    special[2, :3] = [-np.inf, np.inf, np.nan]
+    special[3, :4] = [1e-40, -1e-42, 0.0, -0.0]
+    special[4, :2] = [3.0e38, -3.4e38]
+    x = np.concatenate([x, special])
+    g = torch.tensor([2.0 ** -3], device=cuda) if fmt == "nvfp4" else None
+    m = B.csa_fp4_quantize(torch.from_numpy(x).to(cuda), fmt=fmt, tensor_scale=g)
+    codes, sb = R.encode(x, fmt, None if g is None else g.item())
+    assert np.array_equal(t2np(m.scales), R.block_scales(sb))
+    got = R.unpack(t2np(m.packed))
+    assert np.array_equal(got, codes), np.argwhere(got != codes)[:8]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_encode_strided_rows_and_reused_buffers(B, cuda, dtype):
+    big = torch.randn((3, 40, 200), device=cuda).to(dtype)
+    x = big[:, 4:24, 8:136]  # inner rows 200 apart; the outer step is not 20 of them
+    with pytest.raises(ValueError):
+        B.csa_fp4_quantize(x)
+    x = big[1, :, 8:136]
+    want = B.csa_fp4_quantize(x.contiguous())
+    got = B.csa_fp4_quantize(x, out=B.csa_fp4_quantize(torch.zeros((40, 128), device=cuda)))
+    assert torch.equal(got.packed, want.packed) and torch.equal(got.scales, want.scales)
+    out = torch.full((40, 160), 7.0, dtype=dtype, device=cuda)
+    B.csa_fp4_dequantize(want, out=out[:, 16:144])
+    assert torch.equal(out[:, 16:144], B.csa_fp4_dequantize(want, dtype=dtype))
+    assert (out[:, :16] == 7).all() and (out[:, 144:] == 7).all()
+
+
+LINEAR_SHAPES = [  # M, N, K, G: every tile width, ragged rows, features and K, one to many splits
+    (1, 1, 32, 1), (1, 128, 256, 1), (1, 512, 512, 1), (3, 130, 96, 1), (2, 1024, 8192, 1), (32, 257, 1056, 1),
+    (33, 300, 160, 1), (64, 384, 2080, 1), (65, 129, 4096, 1), (128, 128, 288, 1), (129, 96, 64, 1), (300, 1001, 2080, 1),
+    (513, 640, 544, 1), (5, 128, 128, 3), (257, 384, 640, 2), (700, 256, 384, 4), (40, 256, 4096, 8), (2000, 512, 256, 1)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,G", LINEAR_SHAPES)
+def test_linear_matches_reference(B, cuda, fmt, M, N, K, G):
+    rng = np.random.default_rng(M * 1000003 + N * 101 + K)
+    mx, x = make(B, cuda, rng, M, G * K, fmt)
+    mw, w = make(B, cuda, rng, G * N, K, fmt, K ** -0.5)
+    ref, mag = product(x, w, G)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = B.csa_fp4_linear(mx, mw, groups=G, out_dtype=dtype)
+        assert B.csa_get_device_error() == 0
+        assert_product(y, ref, mag, K, dtype, f"{fmt} {M}x{N}x{K} G={G} {dtype}")
+        assert torch.equal(y, B.csa_fp4_linear(mx, mw, groups=G, out_dtype=dtype)), "not reproducible"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [3, 200])
+def test_linear_into_a_wider_tensor(B, cuda, fmt, M):
+    """Rows of y further apart than its columns: what lies between stays as it was."""
+    rng = np.random.default_rng(M)
+    mx, x = make(B, cuda, rng, M, 256, fmt)
+    mw, w = make(B, cuda, rng, 136, 256, fmt, 0.1)
+    wide = torch.full((M, 151), 3.0, dtype=torch.bfloat16, device=cuda)
+    B.csa_fp4_linear(mx, mw, out=wide[:, :136])
+    assert torch.equal(wide[:, :136], B.csa_fp4_linear(mx, mw)) and (wide[:, 136:] == 3).all()
+
+
+PROJ_SHAPES = [(1, 16, 128, 4, 256, 512), (37, 16, 128, 4, 256, 512), (200, 8, 64, 2, 128, 130), (300, 4, 32, 1, 384, 77)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,H,D,G,Rk,d", PROJ_SHAPES)
+def test_projection_is_its_four_steps(B, cuda, fmt, T, H, D, G, Rk, d):
+    """The projection equals encode, grouped product, encode, product, bit for bit; each of those is
+    held to the 64-bit reference above, and its product to the reference on the encoded z here."""
+    rng = np.random.default_rng(T + H)
+    o = torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).to(cuda).to(torch.bfloat16)
+    A, _ = make(B, cuda, rng, G * Rk, H // G * D, fmt, (H // G * D) ** -0.5)
+    Bm, b64 = make(B, cuda, rng, d, G * Rk, fmt, (G * Rk) ** -0.5)
+    og = torch.tensor([6.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    zg = torch.tensor([40.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    y = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=og, z_scale=zg)
+    z = B.csa_fp4_linear(B.csa_fp4_quantize(o.reshape(T, -1), fmt=fmt, tensor_scale=og), A, groups=G)
+    zq = B.csa_fp4_quantize(z, fmt=fmt, tensor_scale=zg)
+    assert torch.equal(y, B.csa_fp4_linear(zq, Bm))
+    codes, sb = R.encode(z.float().cpu().numpy(), fmt, None if zg is None else zg.item())
+    ref, mag = product(R.decode(codes, sb, fmt, None if zg is None else zg.item()), b64, 1)
+    assert_product(y, ref, mag, G * Rk, torch.bfloat16, "projection")
+    assert B.csa_get_device_error() == 0
+
+
+def test_projection_reuses_its_workspace_on_any_stream(B, cuda):
+    """Two projections with workspaces of their own on two streams at once, each repeated in one
+    workspace, give what each gives alone."""
+    rng = np.random.default_rng(5)
+    A, _ = make(B, cuda, rng, 512, 512, "mxfp4")
+    Bm, _ = make(B, cuda, rng, 256, 512, "mxfp4")
+    o = [torch.randn((T, 8, 128), device=cuda).to(torch.bfloat16) for T in (150, 9)]
+    want = [B.csa_grouped_out_proj_fp4(v, A, Bm, groups=2) for v in o]
+    ws = [torch.empty(B.csa_grouped_out_proj_fp4_workspace("mxfp4", v.shape[0], 8, 128, 2, 256), dtype=torch.uint8, device=cuda)
+          for v in o]
+    streams = [torch.cuda.Stream() for _ in o]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(B.csa_grouped_out_proj_fp4(o[i], A, Bm, groups=2, workspace=ws[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+    with pytest.raises(B.CsaError) as ex:
+        B.csa_grouped_out_proj_fp4(o[0], A, Bm, groups=2, workspace=ws[1])
+    assert ex.value.status == 4
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_captured_and_replayed(B, cuda, fmt):
+    """Encoding, both products and the projection in one CUDA graph, replayed on new inputs."""
+    rng = np.random.default_rng(6)
+    A, _ = make(B, cuda, rng, 256, 256, fmt)
+    Bm, _ = make(B, cuda, rng, 96, 256, fmt)
+    g = torch.tensor([8.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    zg = torch.tensor([300.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    o = torch.zeros((3, 4, 128), dtype=torch.bfloat16, device=cuda)
+
+    def step():
+        q = B.csa_fp4_quantize(o.reshape(3, 512), fmt=fmt, tensor_scale=g)
+        return (B.csa_fp4_dequantize(q), B.csa_fp4_linear(q, A, groups=2),
+                B.csa_grouped_out_proj_fp4(o, A, Bm, groups=2, o_scale=g, z_scale=zg))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for i in range(3):
+        o.copy_(torch.randn(o.shape, device=cuda) * 2)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, step()):
+            assert torch.equal(a, b)
+    assert B.csa_get_device_error() == 0
+
+
+def test_offsets_past_32_bits(B, cuda):
+    """More than 2^32 elements: the last rows of a tall matrix are encoded, decoded and multiplied as
+    the same rows alone are."""
+    rows, cols = 140000, 32768
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=cuda)
+    x[-130:] = torch.randn((130, cols), device=cuda)
+    m = B.csa_fp4_quantize(x)
+    tail = B.csa_fp4_quantize(x[-96:])  # rows - 96 is a whole number of row blocks
+    assert (rows - 96) % 128 == 0
+    assert torch.equal(m.packed[-96:], tail.packed)
+    assert torch.equal(m.scales[-tail.scales.numel():], tail.scales)
+    del x
+    v = B.csa_fp4_dequantize(m)
+    assert torch.equal(v[-96:], B.csa_fp4_dequantize(tail)) and not v[:1000].any()
+    del v
+    w = B.csa_fp4_quantize(torch.randn((160, cols), device=cuda))
+    y = B.csa_fp4_linear(m, w)
+    assert not y[: rows - 130].any()
+    # the same rows alone take another tile width and split: float32 sums in another order
+    a, b = y[-96:].double(), B.csa_fp4_linear(tail, w, out_dtype=torch.float32).double()
+    mag = B.csa_fp4_dequantize(tail).abs().double() @ B.csa_fp4_dequantize(w).abs().double().t()
+    assert ((a - b).abs() <= 2.0 ** -8 * b.abs() + 2 * (cols // 64 + 8) * 2.0 ** -23 * mag).all()
+    assert B.csa_get_device_error() == 0
+
+
+def test_empty_inputs(B, cuda):
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=cuda)
+    m = B.csa_fp4_quantize(x)
+    assert m.packed.shape == (0, 32) and m.scales.numel() == 0
+    assert B.csa_fp4_dequantize(m).shape == (0, 64)
+    w = B.csa_fp4_quantize(torch.ones((32, 64), device=cuda))
+    assert B.csa_fp4_linear(m, w).shape == (0, 32)
+    A = B.csa_fp4_quantize(torch.ones((128, 128), device=cuda))
+    assert B.csa_grouped_out_proj_fp4(torch.empty((0, 2, 64), dtype=torch.bfloat16, device=cuda), A, A, groups=1).shape == (0, 128)
+
+
+def test_nan_and_infinite_scales_reach_only_their_rows(B, cuda):
+    """A NaN scale byte makes its row's products NaN and no other's; a zero row gives zeros."""
+    x = torch.randn((70, 160), device=cuda)
+    x[7] = 0.0
+    m, w = B.csa_fp4_quantize(x), B.csa_fp4_quantize(torch.randn((150, 160), device=cuda))
+    ref = B.csa_fp4_linear(m, w)
+    sc = m.scales.clone()
+    sc[(5 % 32) * 16 + 2] = 255  # row 5, scale 2
+    y = B.csa_fp4_linear(B.Fp4Matrix("mxfp4", 70, 160, m.packed, sc), w)
+    assert y[5].isnan().all() and not ref.isnan().any() and (y[7] == 0).all()
+    keep = torch.arange(70, device=cuda) != 5
+    assert torch.equal(y[keep], ref[keep])
+    sc = w.scales.clone()
+    sc[(3 % 32) * 16 + 1] = 255  # feature 3, scale 1
+    y = B.csa_fp4_linear(m, B.Fp4Matrix("mxfp4", 150, 160, w.packed, sc))
+    keep = torch.arange(150, device=cuda) != 3
+    assert y[:, 3].isnan().all() and torch.equal(y[:, keep], ref[:, keep])
