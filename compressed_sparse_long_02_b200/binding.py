@@ -10,10 +10,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import dataclasses
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -65,6 +65,8 @@ class _Fp4Mat(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """Load libcsa.so (built in-tree by ``__graft_entry__.build()``); raise if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -142,7 +144,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """The current stream of t's device, without the Stream object (2 us of every call)."""
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -411,8 +414,7 @@ _FP4_FMT = {"mxfp4": 0, "nvfp4": 1}
 _FP4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 
 
-@dataclasses.dataclass(frozen=True)
-class Fp4Matrix:
+class Fp4Matrix(NamedTuple):
     """A microscaled 4-bit matrix [rows, cols]: packed uint8 [rows, cols/2], scales uint8 in the
     blocked layout (csa_fp4_scale_bytes bytes) and, for "nvfp4", tensor_scale float32 [1]."""
     fmt: str
@@ -429,6 +431,10 @@ def _fmt(fmt: str) -> int:
     return _FP4_FMT[fmt]
 
 
+def _scale_bytes(fmt: str, rows: int, cols: int) -> int:
+    return (rows + 127) // 128 * (-(-cols // (4 * _FP4_BLOCK[fmt]))) * 512
+
+
 def _tensor_scale(fmt: str, g: torch.Tensor | None, dev, name="tensor_scale"):
     if (g is not None) != (fmt == "nvfp4"):
         raise ValueError(f"{name} goes with nvfp4, and only with it")
@@ -437,42 +443,45 @@ def _tensor_scale(fmt: str, g: torch.Tensor | None, dev, name="tensor_scale"):
     _need(g, torch.float32, None, name)
     if g.numel() != 1 or g.device != dev:
         raise ValueError(f"{name} must be one value on {dev}")
-    return _ptr(g)
+    return g.data_ptr()
 
 
 def _fp4_mat(m: Fp4Matrix, name: str, dev) -> _Fp4Mat:
-    f = _fmt(m.fmt)
-    if m.rows < 0 or m.cols < 32 or m.cols % 32:
-        raise ValueError(f"{name}: cols must be a positive multiple of 32, got {m.cols}")
-    for t, nm in ((m.packed, "packed"), (m.scales, "scales")):
-        _need(t, torch.uint8, None, f"{name}.{nm}")
-        if t.device != dev:
-            raise ValueError(f"{name}.{nm} must be on {dev}, got {t.device}")
-    if m.packed.numel() != m.rows * (m.cols // 2):
-        raise ValueError(f"{name}.packed must hold {m.rows} x {m.cols // 2} bytes, got {m.packed.numel()}")
-    if m.scales.numel() < lib().csa_fp4_scale_bytes(f, m.rows, m.cols):
-        raise ValueError(f"{name}.scales is smaller than csa_fp4_scale_bytes({m.fmt}, {m.rows}, {m.cols})")
-    return _Fp4Mat(_ptr(m.packed), _ptr(m.scales), _tensor_scale(m.fmt, m.tensor_scale, dev, f"{name}.tensor_scale"))
+    fmt, rows, cols, packed, scales, g = m
+    _fmt(fmt)
+    if rows < 0 or cols < 32 or cols % 32:
+        raise ValueError(f"{name}: cols must be a positive multiple of 32, got {cols}")
+    for t, nm in ((packed, "packed"), (scales, "scales")):
+        if t.dtype is not torch.uint8:
+            raise TypeError(f"{name}.{nm} must be torch.uint8, got {t.dtype}")
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}.{nm} must be contiguous on {dev}")
+    if packed.numel() != rows * (cols // 2):
+        raise ValueError(f"{name}.packed must hold {rows} x {cols // 2} bytes, got {packed.numel()}")
+    if scales.numel() < _scale_bytes(fmt, rows, cols):
+        raise ValueError(f"{name}.scales is smaller than csa_fp4_scale_bytes({fmt}, {rows}, {cols})")
+    return _Fp4Mat(packed.data_ptr(), scales.data_ptr(), _tensor_scale(fmt, g, dev, f"{name}.tensor_scale"))
 
 
 def _rows_2d(t: torch.Tensor, name: str):
     """[..., cols] as evenly spaced rows: (rows, cols, elements between rows)."""
-    if t.dim() < 1 or (t.numel() and t.stride(-1) != 1):
+    shape = t.shape
+    if len(shape) == 2 and t.is_contiguous():
+        return shape[0], shape[1], shape[1]
+    if not shape or (t.numel() and t.stride(-1) != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must have contiguous rows")
-    cols = t.shape[-1]
+    cols = shape[-1]
     rows = t.numel() // cols if cols else 0
-    if t.dim() == 1 or rows <= 1:
+    if rows <= 1:
         return rows, cols, cols
-    ld = t.stride(-2) if t.shape[-2] > 1 else 0
-    for i in range(t.dim() - 3, -1, -1):  # every outer dimension must continue the same spacing
-        if t.shape[i] > 1:
-            inner = math.prod(t.shape[i + 1:-1])
+    ld, inner = 0, 1  # the step between rows, and the rows that the dimensions so far span
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] > 1:
             if ld == 0:
-                if t.stride(i) % inner:
-                    raise ValueError(f"{name}'s rows are not evenly spaced")
-                ld = t.stride(i) // inner
-            if t.stride(i) != ld * inner:
+                ld = t.stride(i)
+            elif t.stride(i) != ld * inner:  # an outer dimension must continue the same spacing
                 raise ValueError(f"{name}'s rows are not evenly spaced")
+        inner *= shape[i]
     return rows, cols, ld
 
 
@@ -496,16 +505,17 @@ def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch
     if cols < 32 or cols % 32:
         raise ValueError(f"x's last dimension must be a positive multiple of 32, got {cols}")
     if out is None:
-        out = Fp4Matrix(fmt, rows, cols, torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
-                        torch.empty(lib().csa_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8, device=dev),
-                        tensor_scale)
+        # one allocation: the codes, then the scales from the next multiple of 256 bytes
+        n, at = rows * (cols // 2), (rows * (cols // 2) + 255) // 256 * 256
+        buf = torch.empty(at + _scale_bytes(fmt, rows, cols), dtype=torch.uint8, device=dev)
+        out = Fp4Matrix(fmt, rows, cols, buf[:n].view(rows, cols // 2), buf[at:], tensor_scale)
     elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
         raise ValueError(f"out must be a {fmt} matrix of {rows} x {cols}")
     elif out.tensor_scale is not tensor_scale:
-        out = dataclasses.replace(out, tensor_scale=tensor_scale)
+        out = out._replace(tensor_scale=tensor_scale)
     with _on(x):
         m = _fp4_mat(out, "out", dev)
-        st = lib().csa_fp4_quantize(f, ctypes.c_void_p(x.data_ptr()), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
+        st = lib().csa_fp4_quantize(f, x.data_ptr(), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
     _check("csa_fp4_quantize", st)
     return out
 
@@ -515,13 +525,13 @@ def csa_fp4_dequantize(m: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat16, out
     dev = m.packed.device
     if out is None:
         out = torch.empty((m.rows, m.cols), dtype=dtype, device=dev)
+    dt = _dt(out)
     rows, cols, ld = _rows_2d(out, "out")
-    if (rows, cols) != (m.rows, m.cols) or out.device != dev:
+    if rows != m.rows or cols != m.cols or out.device != dev:
         raise ValueError(f"out must be {m.rows} x {m.cols} on {dev}")
-    with _on(m.packed):
+    with _on(out):
         c = _fp4_mat(m, "m", dev)
-        st = lib().csa_fp4_dequantize(_fmt(m.fmt), ctypes.byref(c), rows, cols, _dt(out), ctypes.c_void_p(out.data_ptr()),
-                                      ld, _stream(out))
+        st = lib().csa_fp4_dequantize(_FP4_FMT[m.fmt], ctypes.byref(c), rows, cols, dt, out.data_ptr(), ld, _stream(out))
     _check("csa_fp4_dequantize", st)
     return out
 
@@ -533,7 +543,7 @@ def csa_fp4_pack_scales(scales: torch.Tensor, cols: int, *, fmt: str = "mxfp4") 
     if cols < 32 or cols % 32 or scales.dim() < 2 or scales.shape[-1] != cols // _FP4_BLOCK[fmt]:
         raise ValueError(f"scales must have {cols} / {_FP4_BLOCK[fmt]} bytes a row, got {tuple(scales.shape)}")
     rows = scales.numel() // scales.shape[-1]
-    out = torch.empty(lib().csa_fp4_scale_bytes(f, rows, cols), dtype=torch.uint8, device=scales.device)
+    out = torch.empty(_scale_bytes(fmt, rows, cols), dtype=torch.uint8, device=scales.device)
     with _on(scales):
         st = lib().csa_fp4_pack_scales(f, _ptr(scales), rows, cols, _ptr(out), _stream(scales))
     _check("csa_fp4_pack_scales", st)
@@ -543,23 +553,21 @@ def csa_fp4_pack_scales(scales: torch.Tensor, cols: int, *, fmt: str = "mxfp4") 
 def csa_fp4_linear(x: Fp4Matrix, w: Fp4Matrix, *, groups: int = 1, out_dtype: torch.dtype = torch.bfloat16,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """x [M, G K] times w [G N, K] group by group -> y [M, G N] (bf16 or float32)."""
-    dev = x.packed.device
-    if x.fmt != w.fmt:
-        raise ValueError(f"x is {x.fmt} and w is {w.fmt}")
-    G, M, K = groups, x.rows, w.cols
+    dev, fmt, G, M, K = x.packed.device, x.fmt, groups, x.rows, w.cols
+    if fmt != w.fmt:
+        raise ValueError(f"x is {fmt} and w is {w.fmt}")
     if G < 1 or w.rows % G or x.cols != G * K:
         raise ValueError(f"x {x.rows} x {x.cols} and w {w.rows} x {w.cols} do not fit {G} groups")
-    N = w.rows // G
     if out is None:
-        out = torch.empty((M, G * N), dtype=out_dtype, device=dev)
+        out = torch.empty((M, w.rows), dtype=out_dtype, device=dev)
     dt = _dt(out)
     rows, cols, ld = _rows_2d(out, "out")
-    if (rows, cols) != (M, G * N) or out.device != dev:
-        raise ValueError(f"out must be {M} x {G * N} on {dev}")
-    with _on(x.packed):
+    if rows != M or cols != w.rows or out.device != dev:
+        raise ValueError(f"out must be {M} x {w.rows} on {dev}")
+    with _on(out):
         cx, cw = _fp4_mat(x, "x", dev), _fp4_mat(w, "w", dev)
-        st = lib().csa_fp4_linear(_fmt(x.fmt), M, N, K, G, ctypes.byref(cx), ctypes.byref(cw), dt,
-                                  ctypes.c_void_p(out.data_ptr()), ld, _stream(x.packed))
+        st = lib().csa_fp4_linear(_FP4_FMT[fmt], M, w.rows // G, K, G, ctypes.byref(cx), ctypes.byref(cw), dt,
+                                  out.data_ptr(), ld, _stream(out))
     _check("csa_fp4_linear", st)
     return out
 
@@ -576,22 +584,22 @@ def csa_grouped_out_proj_fp4(o: torch.Tensor, A: Fp4Matrix, Bm: Fp4Matrix, *, gr
     T, H, D = o.shape
     dev, fmt, G = o.device, A.fmt, groups
     _need(o, torch.bfloat16, None, "o")
-    if A.fmt != Bm.fmt:
-        raise ValueError(f"A is {A.fmt} and Bm is {Bm.fmt}")
+    if fmt != Bm.fmt:
+        raise ValueError(f"A is {fmt} and Bm is {Bm.fmt}")
     if G < 1 or H % G or A.rows % G or A.cols * G != H * D or Bm.cols != A.rows:
         raise ValueError("inconsistent projection shapes")
     R, d_model = A.rows // G, Bm.rows
-    need = csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R)
     if out is None:
         out = torch.empty((T, d_model), dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, (T, d_model), "out")
+    else:
+        _need(out, torch.bfloat16, (T, d_model), "out")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R), dtype=torch.uint8, device=dev)
     if out.device != dev or workspace.device != dev:
         raise ValueError(f"out and workspace must be on {dev}")
     with _on(o):
         ca, cb = _fp4_mat(A, "A", dev), _fp4_mat(Bm, "Bm", dev)
-        st = lib().csa_grouped_out_proj_fp4(_fmt(fmt), T, H, D, G, R, d_model, _ptr(o),
+        st = lib().csa_grouped_out_proj_fp4(_FP4_FMT[fmt], T, H, D, G, R, d_model, _ptr(o),
                                             _tensor_scale(fmt, o_scale, dev, "o_scale"), ctypes.byref(ca),
                                             _tensor_scale(fmt, z_scale, dev, "z_scale"), ctypes.byref(cb), _ptr(out),
                                             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(o))

@@ -2,7 +2,6 @@
 work, the binding refuses what does not fit together, the sizes follow the layout, and the
 tests' reference agrees with the oracle's MXFP4 encoder."""
 import ctypes
-import dataclasses
 
 import numpy as np
 import pytest
@@ -127,8 +126,8 @@ def test_binding_refuses_what_does_not_fit(B):
         B.csa_fp4_pack_scales(u8(4, 3), 64)
     with pytest.raises(TypeError):
         B.csa_fp4_pack_scales(torch.zeros((4, 2)), 64)
-    nv = dataclasses.replace(m, fmt="nvfp4")
-    for x, w, kw in ((m, nv, {}), (m, dataclasses.replace(m, cols=32), {}), (m, m, {"groups": 3}), (m, m, {"groups": 0}),
+    nv = m._replace(fmt="nvfp4")
+    for x, w, kw in ((m, nv, {}), (m, m._replace(cols=32), {}), (m, m, {"groups": 3}), (m, m, {"groups": 0}),
                      (m, m, {"out": torch.zeros((4, 5), dtype=torch.bfloat16)})):
         with pytest.raises(ValueError):
             B.csa_fp4_linear(x, w, **kw)
