@@ -12,11 +12,17 @@
 // streamed once, nothing is padded to 128 rows) and a prefill (kBN = 256).  A K slab is 256
 // elements = 128 bytes a row, one swizzle row.
 //
-// Roles (320 threads): warp 0 issues the loads (codes by TMA boxes, scale atoms by bulk
-// copies), warp 1 owns TMEM and one thread of it copies the slab's scales to TMEM and issues
-// the MMAs, warps 2-9 write the results (two warps per TMEM lane quarter, half of the tile's
-// tokens each; a lane holds one output feature, so a warp's store covers 32 consecutive
-// features of a token).
+// Roles (320 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks),
+// warp 1 owns TMEM and one thread of it copies the slab's scales to TMEM and issues the MMAs,
+// warps 2-9 write the results (two warps per TMEM lane quarter, half of the tile's tokens each;
+// a lane holds one output feature, so a warp's store covers 32 consecutive features of a token).
+//
+// Wide tiles (kPair): the two CTAs of a cluster form one tile of 256 features x 256 tokens
+// (cta_group::2).  Each loads its own 128 features and half of the tokens, so a slab costs an SM
+// 35 KB instead of the 51 KB of a lone 128 x 256 tile; what feeds the FP4 MMAs is L2, at about
+// 83 GB/s per SM, so that ratio is the kernel's speed.  The 256 accumulator columns leave no room
+// for a second accumulator next to the scales: the result warps first read the tile into
+// registers, release it, and convert and store while the next tile's MMAs run.
 //
 // With few tiles the K axis is split over the S CTAs of a cluster: each accumulates its
 // share, puts the float32 partial tile into its shared memory, and CTA r adds the S partials
@@ -41,22 +47,26 @@ constexpr int kThreads = 320;
 constexpr int kEpiThreads = 256;
 constexpr int kSfSlots = 4;          // TMEM slots of scale factors
 
-template <bool kNv, int kBN>
+template <bool kNv, int kBN, bool kPair>
 struct Shape {
+  static_assert(!kPair || kBN == 256, "a pair takes 256 tokens");
+  static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kAtoms = kNv ? 4 : 2;                   // scale atoms of a slab per 128 rows
   static constexpr int kRowBlocks = kBN > 128 ? 2 : 1;         // 128-row scale blocks of the tokens
+  static constexpr int kRowsX = kBN / kCtas;                   // tokens that a CTA loads
   static constexpr uint32_t kBytesW = kTileN * kSlabBytes;     // 16 KB
-  static constexpr uint32_t kBytesX = kBN * kSlabBytes;
+  static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
   static constexpr uint32_t kBytesSf = 512 * kAtoms * (1 + kRowBlocks);
   static constexpr uint32_t kStage = kBytesW + kBytesX + kBytesSf;
-  static constexpr int kStages = static_cast<int>((224u * 1024u) / kStage) < 8 ? static_cast<int>((224u * 1024u) / kStage) : 8;
+  static constexpr int kFit = static_cast<int>((225u * 1024u) / kStage);
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + 512;
   static constexpr int kAcc = kBN > 128 ? 1 : 2;               // accumulators of kBN columns
   static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);  // TMEM columns of a slab's scales
   static constexpr uint32_t kColSf = kAcc * kBN;
   static_assert(kColSf + kSfSlots * kSfCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(kBN * kTileN * 4 <= kStages * kStage, "a partial tile fits in the ring");
+  static_assert(kBN * kTileN * 4 <= kStages * kStage || kPair, "a partial tile fits in the ring");
 };
 
 struct LinearParams {
@@ -64,8 +74,6 @@ struct LinearParams {
   int n_blocks, m_blocks, tiles, splits;
   int x_atoms, w_atoms;   // scale atoms per row block of X and W
   int x_group_atoms;      // atoms of one group's K columns of X
-  const uint8_t* x_scale;
-  const uint8_t* w_scale;
   const float* gx;
   const float* gw;
   void* y;
@@ -82,17 +90,18 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
     static_cast<float*>(y)[at] = v;
 }
 
-template <bool kNv, int kBN, bool kBf16>
+template <bool kNv, int kBN, bool kPair, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                       const LinearParams p) {
-  using S = Shape<kNv, kBN>;
+  using S = Shape<kNv, kBN, kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
   uint8_t* sX = sW + S::kStages * S::kBytesW;
   uint8_t* sSf = sX + S::kStages * S::kBytesX;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSf + S::kStages * S::kBytesSf);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSf + S::kStages * S::kBytesSf);  // of a pair: the leader's are used
   uint64_t* empty = full + S::kStages;
   uint64_t* acc_full = empty + S::kStages;
   uint64_t* acc_empty = acc_full + S::kAcc;
@@ -100,6 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // CTA of the cluster: half of the tile's features in a pair, a share of K otherwise
+  const int per_tile = kPair ? 2 : p.splits;
+  const int rank = static_cast<int>(blockIdx.x) % per_tile;
+  const bool leader = !kPair || rank == 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -108,29 +121,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < S::kAcc; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], 8 * S::kCtas);
     }
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_x);
     prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_xs);
+    prefetch_tmap(&tm_ws);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
+  if constexpr (kPair) cluster_sync_all();  // both CTAs' barriers and TMEM are ready
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_enter();
 
-  const int rank = static_cast<int>(blockIdx.x) % p.splits;
-  const int first = static_cast<int>(blockIdx.x) / p.splits, step = static_cast<int>(gridDim.x) / p.splits;
+  const int first = static_cast<int>(blockIdx.x) / per_tile, step = static_cast<int>(gridDim.x) / per_tile;
   const int slabs = (p.K + kSlab - 1) / kSlab;
-  const int slab0 = static_cast<int>(static_cast<int64_t>(slabs) * rank / p.splits);
-  const int slab1 = static_cast<int>(static_cast<int64_t>(slabs) * (rank + 1) / p.splits);
+  const int slab0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(slabs) * rank / p.splits);
+  const int slab1 = kPair ? slabs : static_cast<int>(static_cast<int64_t>(slabs) * (rank + 1) / p.splits);
+  // tile t: features [n0, n0 + 128) of group g (this CTA's), tokens [m0, m0 + kBN); feature blocks
+  // run fastest, so the CTAs at work share a few token blocks and all weights of L2
+  auto copy_sf = [](uint32_t taddr, uint32_t src) {
+    const uint64_t d = smem_desc(src, 0, 128, kSwizzleNone);
+    if constexpr (kPair)
+      tc_cp_32x128b_warpx4_pair(taddr, d);
+    else
+      tc_cp_32x128b_warpx4(taddr, d);
+  };
+  auto commit = [](uint64_t* bar) {
+    if constexpr (kPair)
+      tc_commit_pair(bar);
+    else
+      tc_commit(bar);
+  };
+  auto tile = [&](int t, int& n0, int& g, int& m0) {
+    const int nb = t % p.n_blocks, mg = t / p.n_blocks;
+    n0 = (nb * S::kCtas + (kPair ? rank : 0)) * kTileN;
+    g = mg % p.G;
+    m0 = mg / p.G * kBN;
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -138,39 +179,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j = 0;
       bool ok = true;
       for (int t = first; ok && t < p.tiles; t += step) {
-        const int nb = t % p.n_blocks, mg = t / p.n_blocks;
-        const int g = mg % p.G, m0 = (mg / p.G) * kBN;
-        const int w_row = g * p.N + nb * kTileN;
-        const int rb_x = m0 / 128;
-        const int rbs = min(S::kRowBlocks, (p.M + 127) / 128 - rb_x);  // a ragged last tile may have one row block less
-        const uint8_t* wsc = p.w_scale + fp4_atom_offset(w_row / 128, 0, p.w_atoms);
-        const uint8_t* xsc = p.x_scale + fp4_atom_offset(rb_x, g * p.x_group_atoms, p.x_atoms);
+        int n0, g, m0;
+        tile(t, n0, g, m0);
+        const int w_row = g * p.N + n0;
+        const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);
+        const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
           if (!mbar_wait(&empty[st], ((j / S::kStages) & 1) ^ 1, p.err, abort_flag)) {
             ok = false;
             break;
           }
-          const int atom0 = sl * S::kAtoms;
-          const uint32_t sf_bytes = 512u * min(S::kAtoms, p.w_atoms - atom0);
-          mbar_arrive_expect_tx(&full[st], S::kBytesW + S::kBytesX + sf_bytes * (1 + rbs));
-          tma_load_2d(smem_u32(sW + st * S::kBytesW), &tm_w, &full[st], sl * kSlabBytes, w_row);
-          tma_load_2d(smem_u32(sX + st * S::kBytesX), &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, m0);
-          const uint32_t dst = smem_u32(sSf + st * S::kBytesSf);
-          bulk_load(dst, wsc + atom0 * 512, sf_bytes, &full[st]);
-          for (int rb = 0; rb < rbs; ++rb)
-            bulk_load(dst + 512 * S::kAtoms * (1 + rb), xsc + fp4_atom_offset(rb, atom0, p.x_atoms), sf_bytes, &full[st]);
+          // codes past K, rows past the ends and scale blocks past the end read as zeros or belong to
+          // columns that no MMA step covers, so every slab counts the same bytes
+          if (leader) mbar_arrive_expect_tx(&full[st], S::kStage * S::kCtas);
+          const int sf0 = sl * S::kAtoms;
+          const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
+          const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
+          if constexpr (kPair) {
+            const uint32_t bar = dsmem_map(&full[st], 0);
+            tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
+            tma_load_2d_pair(dx, &tm_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
+            tma_load_2d_pair(ds, &tm_ws, bar, 0, w_sf + sf0);
+            for (int rb = 0; rb < S::kRowBlocks; ++rb)
+              tma_load_2d_pair(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, bar, 0, x_sf + rb * p.x_atoms + sf0);
+          } else {
+            tma_load_2d(dw, &tm_w, &full[st], sl * kSlabBytes, w_row);
+            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
+            tma_load_2d(ds, &tm_ws, &full[st], 0, w_sf + sf0);
+            for (int rb = 0; rb < S::kRowBlocks; ++rb)
+              tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &full[st], 0, x_sf + rb * p.x_atoms + sf0);
+          }
         }
       }
-      // the last loads issued must have landed before this CTA's shared memory is reused or freed
+      // the last loads issued must have landed before shared memory is reused or freed (of a pair: the
+      // leader waits for both CTAs' bytes, and the other CTA for the leader at the end)
       volatile int never = 0;
-      for (int i = std::max(0, j - S::kStages); i < j; ++i)
-        mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+      if (leader)
+        for (int i = std::max(0, j - S::kStages); i < j; ++i)
+          mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && leader) {
       int j = 0, it = 0;
       bool ok = true;
       for (int t = first; ok && t < p.tiles; t += step, ++it) {
@@ -185,37 +237,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const int left = p.K - sl * kSlab;
-          const int n_mma = min(4, (left + 63) / 64);
-          const int atoms = min(S::kAtoms, p.w_atoms - sl * S::kAtoms);
+          const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
           // scales: W in columns [0, 4 kAtoms) of the slot (4 per atom), then X (4 per atom and row block)
           const uint32_t sfw = tmem + S::kColSf + (j % kSfSlots) * S::kSfCols;
           const uint32_t sfx = sfw + 4 * S::kAtoms;
           const uint32_t src = smem_u32(sSf + st * S::kBytesSf);
-          for (int a = 0; a < atoms; ++a) {
-            tc_cp_32x128b_warpx4(sfw + 4 * a, smem_desc(src + 512 * a, 0, 128, kSwizzleNone));
+#pragma unroll
+          for (int a = 0; a < S::kAtoms; ++a) {
+            copy_sf(sfw + 4 * a, src + 512 * a);
+#pragma unroll
             for (int rb = 0; rb < S::kRowBlocks; ++rb)
-              tc_cp_32x128b_warpx4(sfx + 4 * (S::kRowBlocks * a + rb),
-                                   smem_desc(src + 512 * (S::kAtoms * (1 + rb) + a), 0, 128, kSwizzleNone));
+              copy_sf(sfx + 4 * (S::kRowBlocks * a + rb), src + 512 * (S::kAtoms * (1 + rb) + a));
           }
           const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
-          for (int kk = 0; kk < n_mma; ++kk) {
+          auto mma = [&](int kk) {
             const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
             const uint64_t db = smem_desc(b0 + 32 * kk, 16, 1024, kSwizzle128B);
             const uint32_t accumulate = (sl > slab0 || kk > 0) ? 1u : 0u;
+            constexpr int kRows = kTileN * S::kCtas;
             if constexpr (kNv) {
-              mma_nvf4(acc, da, db, idesc_nvf4(kTileN, kBN), accumulate, sfw + 4 * kk, sfx + 4 * S::kRowBlocks * kk);
+              const uint32_t a = sfw + 4 * kk, b = sfx + 4 * S::kRowBlocks * kk;
+              if constexpr (kPair)
+                mma_nvf4_pair(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
+              else
+                mma_nvf4(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
             } else {
               const uint32_t id = 2 * (kk & 1);  // the byte of the scale column of this K = 64 step
-              mma_mxf4(acc, da, db, idesc_mxf4(kTileN, kBN, id, id), accumulate, (sfw + 4 * (kk >> 1)) | (id << 30),
-                       (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30));
+              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
+              if constexpr (kPair)
+                mma_mxf4_pair(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
+              else
+                mma_mxf4(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
             }
+          };
+          if (n_mma == 4) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma(kk);
+          } else {
+            for (int kk = 0; kk < n_mma; ++kk) mma(kk);
           }
-          tc_commit(&empty[st]);
+          commit(&empty[st]);
         }
-        if (ok) tc_commit(&acc_full[buf]);
+        if (ok) commit(&acc_full[buf]);
       }
-      tc_commit(fin);
+      if constexpr (kPair)
+        tc_commit_pair_local(fin);
+      else
+        tc_commit(fin);
       volatile int never = 0;
       mbar_wait(fin, 0, p.err, &never);
     }
@@ -226,47 +294,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
     float* part = reinterpret_cast<float*>(smem);  // [kBN tokens][128 features], split K only
+    constexpr int kHalf = kBN / 2, kHold = kHalf < 64 ? kHalf : (S::kAcc == 1 ? kHalf : 64);
+    const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
     int it = 0;
     for (int t = first; t < p.tiles; t += step, ++it) {
       const int buf = it % S::kAcc;
       if (!warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag)) break;
       tc_fence_after();
-      const int nb = t % p.n_blocks, mg = t / p.n_blocks;
-      const int g = mg % p.G, m0 = (mg / p.G) * kBN;
-      const int f = 32 * quarter + lane, n = nb * kTileN + f;
-      const int m_left = p.M - m0;
+      int n0, g, m0;
+      tile(t, n0, g, m0);
+      const int f = 32 * quarter + lane, n = n0 + f;
+      // this warp's tokens, kHold of them in registers at a time (all of them when there is one
+      // accumulator, so that the next tile can start before these are stored)
 #pragma unroll 1
-      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 16) {
-        if (c >= m_left) break;
-        uint32_t v[16];
-        tmem_ld16(tmem + lane_base + kBN * buf + c, v);
+      for (int c0 = half * kHalf; c0 < (half + 1) * kHalf; c0 += kHold) {
+        uint32_t v[kHold];
+#pragma unroll
+        for (int c = 0; c < kHold; c += 16) tmem_ld16(tmem + lane_base + kBN * buf + c0 + c, v + c);
         tmem_wait_ld();
-        if (p.splits > 1) {
+        if (c0 + kHold == (half + 1) * kHalf) {  // all read: the MMA may reuse this accumulator
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (kPair)
+              mbar_arrive_cluster(acc_done + 8 * buf);
+            else
+              mbar_arrive(&acc_empty[buf]);
+          }
+        }
+        const int m_left = p.M - m0 - c0;
+        if (!kPair && p.splits > 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * kTileN + f] = __uint_as_float(v[i]);
+          for (int i = 0; i < kHold; ++i) part[(c0 + i) * kTileN + f] = __uint_as_float(v[i]);
         } else if (n < p.N) {
-          const int64_t at = static_cast<int64_t>(m0 + c) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+          const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+          if (m_left >= kHold) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < m_left) store_y<kBf16>(p.y, at + i * p.ldy, __uint_as_float(v[i]) * alpha);
+            for (int i = 0; i < kHold; ++i) store_y<kBf16>(p.y, at + i * p.ldy, __uint_as_float(v[i]) * alpha);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kHold; ++i)
+              if (i < m_left) store_y<kBf16>(p.y, at + i * p.ldy, __uint_as_float(v[i]) * alpha);
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
     }
   }
 
-  if (p.splits > 1) {  // one tile per cluster: every CTA's partial, added in rank order
+  if (!kPair && p.splits > 1) {  // one tile per cluster: every CTA's partial, added in rank order
     cluster_sync_all();
-    const int t = first;
-    const int nb = t % p.n_blocks, mg = t / p.n_blocks;
-    const int g = mg % p.G, m0 = (mg / p.G) * kBN;
+    int n0, g, m0;
+    tile(first, n0, g, m0);
     const int m_valid = min(kBN, p.M - m0);
     const int tok0 = m_valid * rank / p.splits, tok1 = m_valid * (rank + 1) / p.splits;
     const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
     for (int i = threadIdx.x; i < (tok1 - tok0) * (kTileN / 4); i += kThreads) {
-      const int tok = tok0 + i / (kTileN / 4), f = i % (kTileN / 4) * 4, n = nb * kTileN + f;
+      const int tok = tok0 + i / (kTileN / 4), f = i % (kTileN / 4) * 4, n = n0 + f;
       const uint8_t* src = smem + (tok * kTileN + f) * 4;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -295,45 +378,84 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync_all();  // neither CTA leaves while the other's MMAs or loads use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool kNv, int kBN, bool kBf16>
+// Clusters of two that the device holds at once (asked for once per kernel and device).
+template <typename K>
+int resident_pairs(K k, size_t smem, int* cache) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / 2 * 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    cache[dev] = cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : num_sms() / 2;
+  }
+  return cache[dev];
+}
+
+template <bool kNv, int kBN, bool kPair, bool kBf16>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  using Sh = Shape<kNv, kBN>;
-  static int smem_set[64];
-  CUtensorMap tm_x, tm_w;
-  const int64_t xb = static_cast<int64_t>(a.G) * a.K / 2, wb = a.K / 2;
-  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, kBN, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
-  if (!encode_2d_u8(&tm_w, a.w_packed, wb, static_cast<uint64_t>(a.G) * a.N, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B))
+  using Sh = Shape<kNv, kBN, kPair>;
+  static int smem_set[64], pairs[64];
+  CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
+  const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
+  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
+      !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
     return cudaErrorInvalidValue;
   p.m_blocks = (a.M + kBN - 1) / kBN;
+  p.n_blocks = (a.N + kTileN * Sh::kCtas - 1) / (kTileN * Sh::kCtas);
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks * a.G;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
-  // Split K over 2, 4 or 8 CTAs while the tiles leave SMs idle and every CTA keeps two slabs or more.
-  const int slabs = (a.K + kSlab - 1) / kSlab, sms = num_sms();
-  p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= sms && slabs >= 4 * p.splits) p.splits *= 2;
-  const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, sms);
-  auto k = fp4_linear_kernel<kNv, kBN, kBf16>;
+  auto k = fp4_linear_kernel<kNv, kBN, kPair, kBf16>;
   const cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(k), Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(clusters * p.splits)), block(kThreads);
-  if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, p);
-  return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, p);
+  const dim3 block(kThreads);
+  p.splits = 1;
+  if constexpr (kPair) {
+    const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
+    return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, p);
+  } else {
+    // Split K over 2, 4 or 8 CTAs while the tiles leave SMs idle and every CTA keeps two slabs or more.
+    const int slabs = (a.K + kSlab - 1) / kSlab, sms = num_sms();
+    while (p.splits < 8 && tiles * p.splits * 2 <= sms && slabs >= 4 * p.splits) p.splits *= 2;
+    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, sms);
+    const dim3 grid(static_cast<unsigned>(clusters * p.splits));
+    if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, p);
+    return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, p);
+  }
 }
 
 template <bool kNv, bool kBf16>
 cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  // tokens per tile: the smallest that takes them all, 256 beyond
-  if (a.M <= 32) return launch_tile<kNv, 32, kBf16>(a, p, s);
-  if (a.M <= 64) return launch_tile<kNv, 64, kBf16>(a, p, s);
-  if (a.M <= 128) return launch_tile<kNv, 128, kBf16>(a, p, s);
-  return launch_tile<kNv, 256, kBf16>(a, p, s);
+  // tokens per tile: the smallest that takes them all; beyond 128, pairs of CTAs once there is a
+  // tile for every second pair, else lone 256-token tiles whose K axis can be split
+  if (a.M <= 32) return launch_tile<kNv, 32, false, kBf16>(a, p, s);
+  if (a.M <= 64) return launch_tile<kNv, 64, false, kBf16>(a, p, s);
+  if (a.M <= 128) return launch_tile<kNv, 128, false, kBf16>(a, p, s);
+  const int64_t pairs = (static_cast<int64_t>(a.N) + 255) / 256 * ((a.M + 255) / 256) * a.G;
+  if (4 * pairs >= num_sms()) return launch_tile<kNv, 256, true, kBf16>(a, p, s);
+  return launch_tile<kNv, 256, false, kBf16>(a, p, s);
 }
 
 }  // namespace
@@ -345,12 +467,9 @@ cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s) {
   p.N = a.N;
   p.K = a.K;
   p.G = a.G;
-  p.n_blocks = (a.N + kTileN - 1) / kTileN;
   p.x_atoms = fp4_atoms(a.nv, a.G * a.K);
   p.w_atoms = fp4_atoms(a.nv, a.K);
   p.x_group_atoms = a.G > 1 ? p.w_atoms : 0;
-  p.x_scale = a.x_scale;
-  p.w_scale = a.w_scale;
   p.gx = a.gx;
   p.gw = a.gw;
   p.y = a.y;

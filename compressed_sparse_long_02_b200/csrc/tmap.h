@@ -1,5 +1,5 @@
 // tmap.h -- TMA tensor-map encoding through the driver entry point (no link-time
-// dependency on libcuda).  Only 2-D byte tensors are needed by this library.
+// dependency on libcuda).  Only 2-D tensors are needed by this library.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -22,6 +22,20 @@ inline EncodeTiledFn encode_tiled_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(p);
   }
   return fn;
+}
+
+// A list of `rows` 512-byte blocks (uint32 [rows, 128]); box: `box_rows` consecutive blocks,
+// unswizzled.  Blocks past the end read as zeros.
+inline bool encode_blocks_512(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (fn == nullptr || rows == 0) return false;
+  const cuuint64_t dims[2] = {128, rows};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // 2-D uint8 tensor [rows, cols] with row pitch `pitch` bytes; box [box_rows, box_cols].
