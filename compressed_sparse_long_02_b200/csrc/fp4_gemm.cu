@@ -12,10 +12,14 @@
 // streamed once, nothing is padded to 128 rows) and a prefill (kBN = 256).  A K slab is 256
 // elements = 128 bytes a row, one swizzle row.
 //
-// Roles (320 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks),
-// warp 1 owns TMEM and one thread of it copies the slab's scales to TMEM and issues the MMAs,
-// warps 2-9 write the results (two warps per TMEM lane quarter, half of the tile's tokens each;
-// a lane holds one output feature, so a warp's store covers 32 consecutive features of a token).
+// Roles (448 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks);
+// warp 1 owns TMEM and one thread of it issues the MMAs; warps 2-9 write the results (two warps
+// per TMEM lane quarter, half of the tile's tokens each; a lane holds one output feature, so a
+// warp's store covers 32 consecutive features of a token); warps 10-13 bring each slab's scales
+// from shared memory to TMEM.  The scales go by tcgen05.st: a lane's 16 bytes of an atom are its
+// four columns.  tcgen05.cp from the MMA thread runs in order with the MMAs and cost 50-60 cycles
+// per 512-byte atom, 370 (MXFP4) or 650 (NVFP4) cycles next to a 256 x 256 slab's 512 cycles of
+// MMAs; the stores run beside them.
 //
 // Wide tiles (kPair): the two CTAs of a cluster form one tile of 256 features x 256 tokens
 // (cta_group::2).  Each loads its own 128 features and half of the tokens, so a slab costs an SM
@@ -43,9 +47,8 @@ namespace {
 constexpr int kTileN = 128;          // output features of a tile (MMA M)
 constexpr int kSlabBytes = 128;      // bytes of a row in a K slab: 256 elements
 constexpr int kSlab = 2 * kSlabBytes;
-constexpr int kThreads = 320;
-constexpr int kEpiThreads = 256;
-constexpr int kSfSlots = 4;          // TMEM slots of scale factors
+constexpr int kThreads = 448;
+constexpr int kSfWarp = 10;          // first of the four scale warps
 
 template <bool kNv, int kBN, bool kPair>
 struct Shape {
@@ -58,14 +61,19 @@ struct Shape {
   static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
   static constexpr uint32_t kBytesSf = 512 * kAtoms * (1 + kRowBlocks);
   static constexpr uint32_t kStage = kBytesW + kBytesX + kBytesSf;
-  static constexpr int kFit = static_cast<int>((225u * 1024u) / kStage);
+  // Up to 64 tokens (decode) two CTAs share an SM: the next launch's CTAs set up, and wait for
+  // their grid, next to the running ones.
+  static constexpr int kMinBlocks = kBN <= 64 ? 2 : 1;
+  static constexpr int kFit = static_cast<int>((225u * 1024u / kMinBlocks - (kMinBlocks - 1) * 2048u) / kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + 512;
   static constexpr int kAcc = kBN > 128 ? 1 : 2;               // accumulators of kBN columns
   static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);  // TMEM columns of a slab's scales
   static constexpr uint32_t kColSf = kAcc * kBN;
-  static_assert(kColSf + kSfSlots * kSfCols <= 512, "TMEM budget");
-  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static constexpr uint32_t kCols = kColSf + kStages * kSfCols;  // a slot of scales per stage
+  static constexpr uint32_t kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
+  static_assert(kCols <= kTmem && kTmem * kMinBlocks <= 512, "TMEM budget");
+  static_assert((kSmem + 1024) * kMinBlocks <= 228 * 1024, "shared memory budget");
   static_assert(kBN * kTileN * 4 <= kStages * kStage || kPair, "a partial tile fits in the ring");
 };
 
@@ -78,7 +86,7 @@ struct LinearParams {
   const float* gw;
   void* y;
   int64_t ldy;
-  int vec4;               // rows of y allow 4-feature stores
+  int vec2, vec4;         // rows of y allow stores of 2 or 4 features
   int32_t* err;
 };
 
@@ -91,7 +99,7 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 }
 
 template <bool kNv, int kBN, bool kPair, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                       const LinearParams p) {
@@ -103,7 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sSf = sX + S::kStages * S::kBytesX;
   uint64_t* full = reinterpret_cast<uint64_t*>(sSf + S::kStages * S::kBytesSf);  // of a pair: the leader's are used
   uint64_t* empty = full + S::kStages;
-  uint64_t* acc_full = empty + S::kStages;
+  uint64_t* sf_full = empty + S::kStages;      // a stage's scales have landed in this CTA's shared memory
+  uint64_t* sf_ready = sf_full + S::kStages;   // and are in TMEM (of a pair: the leader's are used)
+  uint64_t* acc_full = sf_ready + S::kStages;
   uint64_t* acc_empty = acc_full + S::kAcc;
   uint64_t* fin = acc_empty + S::kAcc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
@@ -118,6 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_ready[s], 4 * S::kCtas);
     }
     for (int b = 0; b < S::kAcc; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -133,10 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) {
     if constexpr (kPair) {
-      tmem_alloc_pair(tmem_slot, 512);
+      tmem_alloc_pair(tmem_slot, S::kTmem);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(tmem_slot, 512);
+      tmem_alloc(tmem_slot, S::kTmem);
       tmem_relinquish();
     }
   }
@@ -153,13 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int slab1 = kPair ? slabs : static_cast<int>(static_cast<int64_t>(slabs) * (rank + 1) / p.splits);
   // tile t: features [n0, n0 + 128) of group g (this CTA's), tokens [m0, m0 + kBN); feature blocks
   // run fastest, so the CTAs at work share a few token blocks and all weights of L2
-  auto copy_sf = [](uint32_t taddr, uint32_t src) {
-    const uint64_t d = smem_desc(src, 0, 128, kSwizzleNone);
-    if constexpr (kPair)
-      tc_cp_32x128b_warpx4_pair(taddr, d);
-    else
-      tc_cp_32x128b_warpx4(taddr, d);
-  };
   auto commit = [](uint64_t* bar) {
     if constexpr (kPair)
       tc_commit_pair(bar);
@@ -192,32 +197,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // codes past K, rows past the ends and scale blocks past the end read as zeros or belong to
           // columns that no MMA step covers, so every slab counts the same bytes
-          if (leader) mbar_arrive_expect_tx(&full[st], S::kStage * S::kCtas);
           const int sf0 = sl * S::kAtoms;
           const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
           const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
+          mbar_arrive_expect_tx(&sf_full[st], S::kBytesSf);
+          tma_load_2d(ds, &tm_ws, &sf_full[st], 0, w_sf + sf0);
+          for (int rb = 0; rb < S::kRowBlocks; ++rb)
+            tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &sf_full[st], 0, x_sf + rb * p.x_atoms + sf0);
+          if (leader) mbar_arrive_expect_tx(&full[st], (S::kBytesW + S::kBytesX) * S::kCtas);
           if constexpr (kPair) {
             const uint32_t bar = dsmem_map(&full[st], 0);
             tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
             tma_load_2d_pair(dx, &tm_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
-            tma_load_2d_pair(ds, &tm_ws, bar, 0, w_sf + sf0);
-            for (int rb = 0; rb < S::kRowBlocks; ++rb)
-              tma_load_2d_pair(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, bar, 0, x_sf + rb * p.x_atoms + sf0);
           } else {
             tma_load_2d(dw, &tm_w, &full[st], sl * kSlabBytes, w_row);
             tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
-            tma_load_2d(ds, &tm_ws, &full[st], 0, w_sf + sf0);
-            for (int rb = 0; rb < S::kRowBlocks; ++rb)
-              tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &full[st], 0, x_sf + rb * p.x_atoms + sf0);
           }
         }
       }
       // the last loads issued must have landed before shared memory is reused or freed (of a pair: the
       // leader waits for both CTAs' bytes, and the other CTA for the leader at the end)
       volatile int never = 0;
-      if (leader)
-        for (int i = std::max(0, j - S::kStages); i < j; ++i)
-          mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+      for (int i = std::max(0, j - S::kStages); i < j; ++i) {
+        mbar_wait(&sf_full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+        if (leader) mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -232,23 +236,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = tmem + kBN * buf;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
-          if (!mbar_wait(&full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
+          const uint32_t ph = (j / S::kStages) & 1;
+          if (!mbar_wait(&sf_ready[st], ph, p.err, abort_flag) || !mbar_wait(&full[st], ph, p.err, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
-          // scales: W in columns [0, 4 kAtoms) of the slot (4 per atom), then X (4 per atom and row block)
-          const uint32_t sfw = tmem + S::kColSf + (j % kSfSlots) * S::kSfCols;
-          const uint32_t sfx = sfw + 4 * S::kAtoms;
-          const uint32_t src = smem_u32(sSf + st * S::kBytesSf);
-#pragma unroll
-          for (int a = 0; a < S::kAtoms; ++a) {
-            copy_sf(sfw + 4 * a, src + 512 * a);
-#pragma unroll
-            for (int rb = 0; rb < S::kRowBlocks; ++rb)
-              copy_sf(sfx + 4 * (S::kRowBlocks * a + rb), src + 512 * (S::kAtoms * (1 + rb) + a));
-          }
+          const uint32_t sfw = tmem + S::kColSf + st * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
           const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
           auto mma = [&](int kk) {
             const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
@@ -288,13 +283,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(fin, 0, p.err, &never);
     }
     __syncwarp();
+  } else if (warp >= kSfWarp) {
+    // ---------------------------------------------------------------- scales to TMEM (warps 10-13)
+    // slot of a stage: W in columns [0, 4 kAtoms) (4 per atom), then X (per atom 4 per row block).
+    // The stage is loaded again only after the MMAs that read the slot, so the slot is free too.
+    const uint32_t dst0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + S::kColSf;
+    const uint32_t ready0 = kPair ? dsmem_map(sf_ready, 0) : 0u;
+    int j = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.tiles; t += step) {
+      for (int sl = slab0; sl < slab1; ++sl, ++j) {
+        const int st = j % S::kStages;
+        if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(sSf + st * S::kBytesSf) + lane;
+        constexpr int kUnits = S::kAtoms * (1 + S::kRowBlocks);
+        uint32_t r[4 * kUnits];
+#pragma unroll
+        for (int a = 0; a < S::kAtoms; ++a) {
+#pragma unroll
+          for (int b = 0; b <= S::kRowBlocks; ++b) {
+            const uint4 u = src[32 * (S::kAtoms * b + a)];
+            uint32_t* d = r + (b == 0 ? 4 * a : 4 * (S::kAtoms + S::kRowBlocks * a + b - 1));
+            d[0] = u.x, d[1] = u.y, d[2] = u.z, d[3] = u.w;
+          }
+        }
+        const uint32_t dst = dst0 + st * S::kSfCols;
+        static_assert(4 * kUnits == 16 || 4 * kUnits == 24 || 4 * kUnits == 32 || 4 * kUnits == 48, "store widths");
+        if constexpr (4 * kUnits >= 32) tmem_st32(dst, r);
+        if constexpr (4 * kUnits % 32 >= 16) tmem_st16(dst + 4 * kUnits / 32 * 32, r + 4 * kUnits / 32 * 32);
+        if constexpr (4 * kUnits % 16 == 8) tmem_st8(dst + 16, r + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_cluster(ready0 + 8 * st);
+          else
+            mbar_arrive(&sf_ready[st]);
+        }
+      }
+    }
   } else {
     // ---------------------------------------------------------------- results (warps 2-9)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
     float* part = reinterpret_cast<float*>(smem);  // [kBN tokens][128 features], split K only
-    constexpr int kHalf = kBN / 2, kHold = kHalf < 64 ? kHalf : (S::kAcc == 1 ? kHalf : 64);
+    constexpr int kHalf = kBN / 2;
     const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
     int it = 0;
     for (int t = first; t < p.tiles; t += step, ++it) {
@@ -304,37 +342,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n0, g, m0;
       tile(t, n0, g, m0);
       const int f = 32 * quarter + lane, n = n0 + f;
-      // this warp's tokens, kHold of them in registers at a time (all of them when there is one
-      // accumulator, so that the next tile can start before these are stored)
-#pragma unroll 1
-      for (int c0 = half * kHalf; c0 < (half + 1) * kHalf; c0 += kHold) {
-        uint32_t v[kHold];
+      const int c0 = half * kHalf;  // this warp's tokens of the tile
+      const uint32_t src = tmem + lane_base + kBN * buf + c0;
+      auto release = [&] {  // all read: the MMA may reuse this accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_cluster(acc_done + 8 * buf);
+          else
+            mbar_arrive(&acc_empty[buf]);
+        }
+      };
+      const int m_left = p.M - m0 - c0;
+      if (!kPair && p.splits > 1) {
 #pragma unroll
-        for (int c = 0; c < kHold; c += 16) tmem_ld16(tmem + lane_base + kBN * buf + c0 + c, v + c);
-        tmem_wait_ld();
-        if (c0 + kHold == (half + 1) * kHalf) {  // all read: the MMA may reuse this accumulator
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (kPair)
-              mbar_arrive_cluster(acc_done + 8 * buf);
-            else
-              mbar_arrive(&acc_empty[buf]);
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(src + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(c0 + c + i) * kTileN + f] = __uint_as_float(v[i]);
+        }
+        release();
+        continue;
+      }
+      const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+      if constexpr (kBf16) {
+        // the warp's whole share rounded into registers, then stored while the next tile runs
+        uint32_t v[kHalf / 2];
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t u[16];
+          tmem_ld16(src + c, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[c / 2 + i] = fp4_bf16x2(__uint_as_float(u[2 * i]) * alpha, __uint_as_float(u[2 * i + 1]) * alpha);
+        }
+        release();
+        if (p.vec2) {
+          // lanes 2i and 2i + 1 trade: the even lane stores both features of the even token, the odd
+          // lane those of the odd token, four bytes each
+          const int odd = lane & 1;
+          char* y = static_cast<char*>(p.y) + 2 * (at - odd + odd * p.ldy);
+          const int64_t step_y = 4 * p.ldy;
+          const bool in = n - odd < p.N;
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, v[i], 1);
+            const uint32_t w = odd ? __byte_perm(o, v[i], 0x7632) : __byte_perm(v[i], o, 0x5410);
+            if (in && 2 * i + odd < m_left) *reinterpret_cast<uint32_t*>(y) = w;
+            y += step_y;
+          }
+        } else if (n < p.N) {
+          uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            if (i < m_left) *y = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+            y += p.ldy;
           }
         }
-        const int m_left = p.M - m0 - c0;
-        if (!kPair && p.splits > 1) {
+      } else {
+        float* y = static_cast<float*>(p.y) + at;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t u[16];
+          tmem_ld16(src + c, u);
+          tmem_wait_ld();
+          if (c + 16 == kHalf) release();
+          if (n < p.N) {
 #pragma unroll
-          for (int i = 0; i < kHold; ++i) part[(c0 + i) * kTileN + f] = __uint_as_float(v[i]);
-        } else if (n < p.N) {
-          const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
-          if (m_left >= kHold) {
-#pragma unroll
-            for (int i = 0; i < kHold; ++i) store_y<kBf16>(p.y, at + i * p.ldy, __uint_as_float(v[i]) * alpha);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kHold; ++i)
-              if (i < m_left) store_y<kBf16>(p.y, at + i * p.ldy, __uint_as_float(v[i]) * alpha);
+            for (int i = 0; i < 16; ++i)
+              if (c + i < m_left) y[(c + i) * p.ldy] = __uint_as_float(u[i]) * alpha;
           }
         }
       }
@@ -382,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     if constexpr (kPair)
-      tmem_dealloc_pair(tmem, 512);
+      tmem_dealloc_pair(tmem, S::kTmem);
     else
-      tmem_dealloc(tmem, 512);
+      tmem_dealloc(tmem, S::kTmem);
   }
 }
 
@@ -436,10 +516,10 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s)
     const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
     return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, p);
   } else {
-    // Split K over 2, 4 or 8 CTAs while the tiles leave SMs idle and every CTA keeps two slabs or more.
-    const int slabs = (a.K + kSlab - 1) / kSlab, sms = num_sms();
-    while (p.splits < 8 && tiles * p.splits * 2 <= sms && slabs >= 4 * p.splits) p.splits *= 2;
-    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, sms);
+    // Split K over 2, 4 or 8 CTAs while the tiles leave SMs (or half SMs) idle and every CTA keeps two slabs or more.
+    const int slabs = (a.K + kSlab - 1) / kSlab, room = num_sms();
+    while (p.splits < 8 && tiles * p.splits * 2 <= room && slabs >= 4 * p.splits) p.splits *= 2;
+    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, room);
     const dim3 grid(static_cast<unsigned>(clusters * p.splits));
     if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, p);
     return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, p);
@@ -474,6 +554,7 @@ cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s) {
   p.gw = a.gw;
   p.y = a.y;
   p.ldy = a.ldy;
+  p.vec2 = a.N % 2 == 0 && a.ldy % 2 == 0;
   p.vec4 = a.N % 4 == 0 && a.ldy % 4 == 0;
   p.err = device_error_word();
   if (p.err == nullptr) return cudaErrorUnknown;
