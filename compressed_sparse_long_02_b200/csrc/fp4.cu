@@ -19,7 +19,6 @@
 
 #include "fp4.cuh"
 #include "internal.h"
-#include "mxfp4.cuh"
 #include "ptx.cuh"
 
 namespace csa {
@@ -27,19 +26,6 @@ namespace {
 
 constexpr int kFp4Threads = 256;
 constexpr int kChunk = 256;  // columns of a warp's task: 8 per lane
-
-// NVFP4 scale byte of a block: e4m3(amax / (6 g)), to nearest even, at most 448
-__device__ __forceinline__ uint32_t nv_scale_byte(float amax, float six_g) {
-  return __nv_cvt_float_to_fp8(__fdiv_rn(amax, six_g), __NV_SATFINITE, __NV_E4M3);
-}
-
-// Codes of eight values under the NVFP4 scale T: e2m1(x / T), zeros if T is zero
-__device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T) {
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = T > 0.f ? __fdiv_rn(v[i], T) : 0.f;
-  return e2m1x8_rn(y, 1.f);
-}
 
 struct Fp4Shape {
   int64_t rows;

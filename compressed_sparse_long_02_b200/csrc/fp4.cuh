@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "mxfp4.cuh"
+
 namespace csa {
 
 __host__ __device__ constexpr int fp4_block(bool nv) { return nv ? 16 : 32; }  // elements per scale
@@ -23,6 +25,19 @@ __host__ __device__ constexpr int64_t fp4_atom_offset(int64_t row_block, int ato
 
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {  // exact; 0x7F / 0xFF are NaN
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
+}
+
+// NVFP4 scale byte of a block: e4m3(amax / (6 g)), to nearest even, at most 448
+__device__ __forceinline__ uint32_t nv_scale_byte(float amax, float six_g) {
+  return __nv_cvt_float_to_fp8(__fdiv_rn(amax, six_g), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Codes of eight values under the NVFP4 scale T: e2m1(x / T), zeros if T is zero
+__device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = T > 0.f ? __fdiv_rn(v[i], T) : 0.f;
+  return e2m1x8_rn(y, 1.f);
 }
 
 // 2^(byte - 127); byte 255 is NaN, byte 0 the subnormal 2^-127
@@ -67,6 +82,12 @@ __device__ __forceinline__ void fp4_load8(const void* x, int64_t at, float (&v)[
 __device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// larger of two pairs of bf16, NaNs left out
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 template <bool kBf16>

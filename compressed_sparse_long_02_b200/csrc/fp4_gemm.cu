@@ -8,29 +8,32 @@
 // (tcgen05.mma kind::mxf4 / kind::mxf4nvf4, block_scale), accumulating in float32 in TMEM.
 //
 // The weights go on the MMA's M axis (128 output features a tile) and the tokens on its N
-// axis (kBN a tile), so one kernel serves a single decode token (kBN = 32: the weights are
-// streamed once, nothing is padded to 128 rows) and a prefill (kBN = 256).  A K slab is 256
-// elements = 128 bytes a row, one swizzle row.
+// axis (kBN a tile), so a single decode token (kBN = 32) streams the weights once and pads
+// nothing to 128 rows.  A K slab is 256 elements = 128 bytes a row, one swizzle row.
 //
 // Roles (448 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks);
 // warp 1 owns TMEM and one thread of it issues the MMAs; warps 2-9 write the results (two warps
-// per TMEM lane quarter, half of the tile's tokens each; a lane holds one output feature, so a
-// warp's store covers 32 consecutive features of a token); warps 10-13 bring each slab's scales
-// from shared memory to TMEM.  The scales go by tcgen05.st: a lane's 16 bytes of an atom are its
-// four columns.  tcgen05.cp from the MMA thread runs in order with the MMAs and cost 50-60 cycles
-// per 512-byte atom, 370 (MXFP4) or 650 (NVFP4) cycles next to a 256 x 256 slab's 512 cycles of
-// MMAs; the stores run beside them.
+// per TMEM lane quarter, half of the tile's tokens each; a lane holds one output feature);
+// warps 10-13 bring each slab's scales from shared memory to TMEM.  The scales go by
+// tcgen05.st: a lane's 16 bytes of an atom are its four columns.  tcgen05.cp from the MMA thread
+// runs in order with the MMAs and cost 50-60 cycles per 512-byte atom, 370 (MXFP4) or 650
+// (NVFP4) cycles next to a 256 x 256 slab's 512 cycles of MMAs; the stores run beside them.
 //
-// Wide tiles (kPair): the two CTAs of a cluster form one tile of 256 features x 256 tokens
+// Pairs (kBN = 256): the two CTAs of a cluster form one tile of 256 features x 256 tokens
 // (cta_group::2).  Each loads its own 128 features and half of the tokens, so a slab costs an SM
 // 35 KB instead of the 51 KB of a lone 128 x 256 tile; what feeds the FP4 MMAs is L2, at about
 // 83 GB/s per SM, so that ratio is the kernel's speed.  The 256 accumulator columns leave no room
 // for a second accumulator next to the scales: the result warps first read the tile into
 // registers, release it, and convert and store while the next tile's MMAs run.
 //
-// With few tiles the K axis is split over the S CTAs of a cluster: each accumulates its
-// share, puts the float32 partial tile into its shared memory, and CTA r adds the S partials
-// of its tokens in rank order (the sum does not depend on timing).
+// Lone CTAs (kBN <= 128): with few tiles the K axis is split over the S CTAs of a cluster.  Each
+// CTA sends every other its float32 partial sums of that CTA's tokens (asynchronous stores into
+// its shared memory, counted on a barrier), and each adds the S partials of its tokens in rank
+// order, so the sum does not depend on timing.  Before it waits for the previous grid, a CTA asks
+// for its weights in L2: a hint, which reads nothing, so it may run ahead of whatever wrote them.
+//
+// Results are float32 or bf16, or (the projection's intermediate) rounded to bf16 and encoded
+// again: the scales' blocks run along the features, which a warp's lanes hold.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,6 +41,7 @@
 
 #include "fp4.cuh"
 #include "internal.h"
+#include "mxfp4.cuh"
 #include "ptx.cuh"
 #include "tmap.h"
 
@@ -50,9 +54,11 @@ constexpr int kSlab = 2 * kSlabBytes;
 constexpr int kThreads = 448;
 constexpr int kSfWarp = 10;          // first of the four scale warps
 
-template <bool kNv, int kBN, bool kPair>
+enum Out { kOutF32, kOutBf16, kOutFp4 };
+
+template <bool kNv, int kBN, int kOut>
 struct Shape {
-  static_assert(!kPair || kBN == 256, "a pair takes 256 tokens");
+  static constexpr bool kPair = kBN == 256;
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kAtoms = kNv ? 4 : 2;                   // scale atoms of a slab per 128 rows
   static constexpr int kRowBlocks = kBN > 128 ? 2 : 1;         // 128-row scale blocks of the tokens
@@ -61,20 +67,21 @@ struct Shape {
   static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
   static constexpr uint32_t kBytesSf = 512 * kAtoms * (1 + kRowBlocks);
   static constexpr uint32_t kStage = kBytesW + kBytesX + kBytesSf;
+  // lone CTAs: float32 partials, all CTAs', of this CTA's tokens; pairs: 2 x 64 tokens to encode
+  static constexpr uint32_t kRecv = kPair ? (kOut == kOutFp4 ? 2 * 64 * kTileN * 2 : 0) : kBN * kTileN * 4;
   // Up to 64 tokens (decode) two CTAs share an SM: the next launch's CTAs set up, and wait for
   // their grid, next to the running ones.
   static constexpr int kMinBlocks = kBN <= 64 ? 2 : 1;
-  static constexpr int kFit = static_cast<int>((225u * 1024u / kMinBlocks - (kMinBlocks - 1) * 2048u) / kStage);
+  static constexpr int kFit = static_cast<int>(((kMinBlocks == 2 ? 111u : 225u) * 1024u - kRecv) / kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + 512;
-  static constexpr int kAcc = kBN > 128 ? 1 : 2;               // accumulators of kBN columns
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kRecv + 512;
+  static constexpr int kAcc = kPair ? 1 : 2;                   // accumulators of kBN columns
   static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);  // TMEM columns of a slab's scales
   static constexpr uint32_t kColSf = kAcc * kBN;
   static constexpr uint32_t kCols = kColSf + kStages * kSfCols;  // a slot of scales per stage
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= kTmem && kTmem * kMinBlocks <= 512, "TMEM budget");
   static_assert((kSmem + 1024) * kMinBlocks <= 228 * 1024, "shared memory budget");
-  static_assert(kBN * kTileN * 4 <= kStages * kStage || kPair, "a partial tile fits in the ring");
 };
 
 struct LinearParams {
@@ -87,35 +94,139 @@ struct LinearParams {
   void* y;
   int64_t ldy;
   int vec2, vec4;         // rows of y allow stores of 2 or 4 features
+  uint8_t* z_packed;      // kOutFp4: codes [M, G N / 2], scales, tensor scale
+  uint8_t* z_scale;
+  const float* gz;
+  int z_atoms;
   int32_t* err;
 };
 
-template <bool kBf16>
+template <int kOut>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
-  if constexpr (kBf16)
+  if constexpr (kOut == kOutBf16)
     static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
   else
     static_cast<float*>(y)[at] = v;
 }
 
-template <bool kNv, int kBN, bool kPair, bool kBf16>
-__global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
+__device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+// byte of the scale (token m, block blk) in a blocked layout of n_atoms atoms per row block
+__device__ __forceinline__ int64_t scale_at(int m, int blk, int n_atoms) {
+  return fp4_atom_offset(m / 128, blk / 4, n_atoms) + (m % 32) * 16 + (m % 128) / 32 * 4 + blk % 4;
+}
+
+// The pair's encoding of 64 tokens x 128 features goes through shared memory, where a row of 128
+// bf16 features is sixteen 16-byte chunks, placed so that both a warp's writes (32 features of two
+// tokens) and its reads (32 features of each of eight tokens per chunk) spread over the banks.
+__device__ __forceinline__ int z_chunk(int tok, int c) { return tok * 16 + (c ^ ((c >> 3) & 1) ^ ((tok & 1) << 1)); }
+
+// Encodes 32 consecutive features (feat, a multiple of 32) of one bf16 token; four neighbouring
+// lanes hold the four quarters of 128 features of one token and join their scale bytes.
+template <bool kNv>
+__device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, int feat, int n_feat, int n_atoms,
+                                          const LinearParams& p, float g) {
+  const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
+                          x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
+  uint32_t codes[4], bytes = 0;
+  float inv[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // halves of 16: a block each (NVFP4) or together (MXFP4)
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) am = bf16x2_max(am, w[8 * h + i] & 0x7FFF7FFFu);
+    inv[h] = fmaxf(__uint_as_float(am << 16), __uint_as_float(am & 0xFFFF0000u));
+  }
+  if constexpr (kNv) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t byte = nv_scale_byte(inv[h], 6.f * g);
+      bytes |= byte << (8 * h);
+      inv[h] = e4m3_value(byte) * g;  // T
+    }
+  } else {
+    const int E = mx_block_exponent(fmaxf(inv[0], inv[1]));
+    bytes = E + 127;
+    inv[0] = inv[1] = mx_pow2_neg(E);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[4 * q + i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[4 * q + i] & 0xFFFF0000u);
+    }
+    codes[q] = kNv ? nv_codes8(v, inv[q / 2]) : e2m1x8_rn(v, inv[q / 2]);
+  }
+  const int lane = threadIdx.x & 31;
+  if constexpr (kNv) {  // two bytes per lane: lanes 0, 1 hold one atom's four scales, lanes 2, 3 the next's
+    bytes <<= 16 * (lane & 1);
+    bytes |= __shfl_xor_sync(0xffffffffu, bytes, 1);
+  } else {
+    bytes <<= 8 * (lane & 3);
+    bytes |= __shfl_xor_sync(0xffffffffu, bytes, 1);
+    bytes |= __shfl_xor_sync(0xffffffffu, bytes, 2);
+  }
+  if (in) {
+    *reinterpret_cast<uint4*>(p.z_packed + (static_cast<int64_t>(m) * n_feat + feat) / 2) =
+        make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    if (lane % (kNv ? 2 : 4) == 0)
+      *reinterpret_cast<uint32_t*>(p.z_scale + scale_at(m, feat / (kNv ? 16 : 32), n_atoms)) = bytes;
+  }
+}
+
+// Encodes four features (n_feat per row) of one token: a warp holds 128 consecutive features.
+template <bool kNv>
+__device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat, int n_feat, int n_atoms,
+                                           const LinearParams& p, float g) {
+  float x[4], am = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[e] = bf16_round(o[e]);
+    am = fmaxf(am, fabsf(x[e]));
+  }
+  constexpr int kBlk = kNv ? 16 : 32;
+#pragma unroll
+  for (int d = 1; d < kBlk / 4; d <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, d));
+  uint32_t byte, codes;
+  if constexpr (kNv) {
+    byte = nv_scale_byte(am, 6.f * g);
+    const float T = e4m3_value(byte) * g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = T > 0.f ? __fdiv_rn(x[e], T) : 0.f;
+    codes = e2m1x2_rn(x[0], x[1]) | e2m1x2_rn(x[2], x[3]) << 8;
+  } else {
+    const int E = mx_block_exponent(am);
+    const float s = mx_pow2_neg(E);
+    byte = E + 127;
+    codes = e2m1x2_rn(x[0] * s, x[1] * s) | e2m1x2_rn(x[2] * s, x[3] * s) << 8;
+  }
+  reinterpret_cast<uint16_t*>(p.z_packed)[(static_cast<int64_t>(m) * n_feat + feat) / 4] = static_cast<uint16_t>(codes);
+  if (feat % kBlk == 0) p.z_scale[scale_at(m, feat / kBlk, n_atoms)] = static_cast<uint8_t>(byte);
+}
+
+template <bool kNv, int kBN, int kOut>
+__global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                       const LinearParams p) {
-  using S = Shape<kNv, kBN, kPair>;
+  using S = Shape<kNv, kBN, kOut>;
+  constexpr bool kPair = S::kPair;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
   uint8_t* sX = sW + S::kStages * S::kBytesW;
   uint8_t* sSf = sX + S::kStages * S::kBytesX;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSf + S::kStages * S::kBytesSf);  // of a pair: the leader's are used
+  float* recv = reinterpret_cast<float*>(sSf + S::kStages * S::kBytesSf);  // [CTA][token][128 features]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(recv) + S::kRecv);  // of a pair: the leader's are used
   uint64_t* empty = full + S::kStages;
   uint64_t* sf_full = empty + S::kStages;      // a stage's scales have landed in this CTA's shared memory
   uint64_t* sf_ready = sf_full + S::kStages;   // and are in TMEM (of a pair: the leader's are used)
   uint64_t* acc_full = sf_ready + S::kStages;
   uint64_t* acc_empty = acc_full + S::kAcc;
-  uint64_t* fin = acc_empty + S::kAcc;
+  uint64_t* recv_full = acc_empty + S::kAcc;
+  uint64_t* fin = recv_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 8 * S::kCtas);
     }
+    mbar_init(recv_full, 1);
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -153,11 +265,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
     }
   }
   tc_fence_before();
-  if constexpr (kPair) cluster_sync_all();  // both CTAs' barriers and TMEM are ready
+  if (per_tile > 1) cluster_sync_all();  // every CTA's barriers (and a pair's TMEM) are ready
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_enter();
 
   const int first = static_cast<int>(blockIdx.x) / per_tile, step = static_cast<int>(gridDim.x) / per_tile;
   const int slabs = (p.K + kSlab - 1) / kSlab;
@@ -177,6 +288,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
     g = mg % p.G;
     m0 = mg / p.G * kBN;
   };
+
+  if (threadIdx.x == 0 && first < p.tiles) {
+    int n0, g, m0;
+    tile(first, n0, g, m0);
+    const int w_row = g * p.N + n0, n = min(slab1 - slab0, 4 * S::kStages);
+    for (int i = 0; i < n; ++i) tma_prefetch_2d(&tm_w, (slab0 + i) * kSlabBytes, w_row);
+    for (int i = 0; i < n; ++i) tma_prefetch_2d(&tm_ws, 0, w_row / 128 * p.w_atoms + (slab0 + i) * S::kAtoms);
+  }
+  griddep_enter();
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -329,21 +449,26 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
   } else {
     // ---------------------------------------------------------------- results (warps 2-9)
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
-    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
-    float* part = reinterpret_cast<float*>(smem);  // [kBN tokens][128 features], split K only
     constexpr int kHalf = kBN / 2;
+    const int f = 32 * quarter + lane, c0 = half * kHalf;  // this lane's feature, this warp's first token of a tile
+    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+    const float gz = kOut == kOutFp4 && kNv ? __ldg(p.gz) : 1.f;
     const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
+    if (!kPair && p.splits > 1 && warp == 2 && lane == 0) {  // the bytes this CTA will receive
+      int n0, g, m0;
+      tile(first, n0, g, m0);
+      const int m_valid = min(kBN, p.M - m0), cap = (m_valid + p.splits - 1) / p.splits;
+      mbar_arrive_expect_tx(recv_full, max(0, min(cap, m_valid - rank * cap)) * kTileN * 4 * p.splits);
+    }
     int it = 0;
     for (int t = first; t < p.tiles; t += step, ++it) {
       const int buf = it % S::kAcc;
-      if (!warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag)) break;
+      const bool got = warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag);
+      if (!got && (kPair || p.splits > 1)) break;  // a lone CTA's warps meet below, whatever each saw
       tc_fence_after();
       int n0, g, m0;
       tile(t, n0, g, m0);
-      const int f = 32 * quarter + lane, n = n0 + f;
-      const int c0 = half * kHalf;  // this warp's tokens of the tile
-      const uint32_t src = tmem + lane_base + kBN * buf + c0;
+      const uint32_t src = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + kBN * buf + c0;
       auto release = [&] {  // all read: the MMA may reuse this accumulator
         tc_fence_before();
         __syncwarp();
@@ -354,22 +479,73 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
             mbar_arrive(&acc_empty[buf]);
         }
       };
-      const int m_left = p.M - m0 - c0;
-      if (!kPair && p.splits > 1) {
+      const int m_valid = min(kBN, p.M - m0), m_left = m_valid - c0;  // tokens of the tile; of this warp's share
+      if constexpr (!kPair) {
+        // float32 sums to the CTA that writes the token: itself, or over the cluster
+        const int cap = (m_valid + p.splits - 1) / p.splits;
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(src + c, v);
+          if (c >= m_left) break;
+          uint32_t u[16];
+          tmem_ld16(src + c, u);
           tmem_wait_ld();
+          if (p.splits == 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c0 + c + i) * kTileN + f] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) recv[(c0 + c + i) * kTileN + f] = __uint_as_float(u[i]);
+          } else {
+            int r = (c0 + c) / cap, i0 = c0 + c - r * cap;  // the token's CTA, its place there
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c + i < m_left) st_async_u32(dsmem_map(recv + (rank * cap + i0) * kTileN + f, r), u[i], dsmem_map(recv_full, r));
+              if (++i0 == cap) i0 = 0, ++r;
+            }
+          }
         }
         release();
-        continue;
-      }
-      const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
-      if constexpr (kBf16) {
-        // the warp's whole share rounded into registers, then stored while the next tile runs
+        if (p.splits == 1 ? named_bar_or(1, 256, !got) : !warp_wait(recv_full, 0, p.err, abort_flag)) break;
+        // a warp takes a token at a time: four features per lane, the partials added in rank order
+        const int tok0 = p.splits > 1 ? rank * cap : 0, n_tok = p.splits > 1 ? min(cap, m_valid - rank * cap) : m_valid;
+        for (int i = warp - 2; i < n_tok; i += 8) {
+          const float* part = recv + i * kTileN + 4 * lane;
+          float4 sum = *reinterpret_cast<const float4*>(part);
+          for (int r = 1; r < p.splits; ++r) {
+            const float4 q = *reinterpret_cast<const float4*>(part + r * cap * kTileN);
+            sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
+          }
+          const float o[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
+          const int m = m0 + tok0 + i, n = n0 + 4 * lane;
+          const int64_t at = static_cast<int64_t>(m) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+          if constexpr (kOut == kOutFp4) {
+            encode_row<kNv>(o, m, g * p.N + n, p.G * p.N, p.z_atoms, p, gz);
+          } else if (p.vec4 && n + 3 < p.N) {
+            if constexpr (kOut == kOutBf16)
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(fp4_bf16x2(o[0], o[1]), fp4_bf16x2(o[2], o[3]));
+            else
+              *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.N) store_y<kOut>(p.y, at + e, o[e]);
+          }
+        }
+        if (p.splits == 1) named_bar_sync(1, 256);  // the buffer is free for the next tile
+      } else if constexpr (kOut == kOutF32) {
+        const int n = n0 + f;
+        float* y = static_cast<float*>(p.y) + static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t u[16];
+          tmem_ld16(src + c, u);
+          tmem_wait_ld();
+          if (c + 16 == kHalf) release();
+          if (n < p.N) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < m_left) y[(c + i) * p.ldy] = __uint_as_float(u[i]) * alpha;
+          }
+        }
+      } else {
+        // the warp's whole share rounded to bf16 in registers, then stored while the next tile runs
         uint32_t v[kHalf / 2];
 #pragma unroll
         for (int c = 0; c < kHalf; c += 16) {
@@ -381,7 +557,34 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
             v[c / 2 + i] = fp4_bf16x2(__uint_as_float(u[2 * i]) * alpha, __uint_as_float(u[2 * i + 1]) * alpha);
         }
         release();
-        if (p.vec2) {
+        const int n = n0 + f;
+        const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
+        if constexpr (kOut == kOutFp4) {
+          // 64 tokens at a time among the four warps of this half, whose lanes hold all 128 features
+          uint4* buf_z = reinterpret_cast<uint4*>(recv) + half * 64 * 16;
+          uint32_t* buf_w = reinterpret_cast<uint32_t*>(buf_z);
+          const int odd = lane & 1, id = (warp - 2) % 4 * 32 + lane;
+#pragma unroll
+          for (int part = 0; part < kHalf / 64; ++part) {
+            named_bar_sync(1 + half, 128);  // the last readers are done
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t x = v[32 * part + i], o = __shfl_xor_sync(0xffffffffu, x, 1);
+              buf_w[4 * z_chunk(2 * i + odd, f >> 3) + ((f >> 1) & 3)] = odd ? __byte_perm(o, x, 0x7632) : __byte_perm(x, o, 0x5410);
+            }
+            named_bar_sync(1 + half, 128);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int tok = u * 32 + id / 4, b = id % 4;
+              uint4 x[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = buf_z[z_chunk(tok, 4 * b + j)];
+              const int in_tile = 64 * part + tok;
+              encode_32<kNv>(x, in_tile < m_left && n0 < p.N, m0 + c0 + in_tile, g * p.N + n0 + 32 * b, p.G * p.N,
+                             p.z_atoms, p, gz);
+            }
+          }
+        } else if (p.vec2) {
           // lanes 2i and 2i + 1 trade: the even lane stores both features of the even token, the odd
           // lane those of the odd token, four bytes each
           const int odd = lane & 1;
@@ -403,59 +606,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kPair>::kMinBlocks)
             y += p.ldy;
           }
         }
-      } else {
-        float* y = static_cast<float*>(p.y) + at;
-#pragma unroll 1
-        for (int c = 0; c < kHalf; c += 16) {
-          uint32_t u[16];
-          tmem_ld16(src + c, u);
-          tmem_wait_ld();
-          if (c + 16 == kHalf) release();
-          if (n < p.N) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < m_left) y[(c + i) * p.ldy] = __uint_as_float(u[i]) * alpha;
-          }
-        }
       }
     }
   }
 
-  if (!kPair && p.splits > 1) {  // one tile per cluster: every CTA's partial, added in rank order
-    cluster_sync_all();
-    int n0, g, m0;
-    tile(first, n0, g, m0);
-    const int m_valid = min(kBN, p.M - m0);
-    const int tok0 = m_valid * rank / p.splits, tok1 = m_valid * (rank + 1) / p.splits;
-    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
-    for (int i = threadIdx.x; i < (tok1 - tok0) * (kTileN / 4); i += kThreads) {
-      const int tok = tok0 + i / (kTileN / 4), f = i % (kTileN / 4) * 4, n = n0 + f;
-      const uint8_t* src = smem + (tok * kTileN + f) * 4;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int r = 0; r < p.splits; ++r) {
-        const uint4 u = dsmem_ld4(dsmem_map(src, r));
-        sum.x += __uint_as_float(u.x);
-        sum.y += __uint_as_float(u.y);
-        sum.z += __uint_as_float(u.z);
-        sum.w += __uint_as_float(u.w);
-      }
-      const float o[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
-      const int64_t at = static_cast<int64_t>(m0 + tok) * p.ldy + static_cast<int64_t>(g) * p.N + n;
-      if (p.vec4 && n + 3 < p.N) {
-        if constexpr (kBf16)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(fp4_bf16x2(o[0], o[1]), fp4_bf16x2(o[2], o[3]));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < p.N) store_y<kBf16>(p.y, at + e, o[e]);
-      }
-    }
-    cluster_sync_all();  // no CTA leaves while another still reads its partial
+  // no CTA leaves before every CTA of its cluster has sent its partials
+  if (!kPair && p.splits > 1) {
+    __syncwarp();
+    cluster_arrive_relaxed();
+    cluster_wait();
   }
-
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync_all();  // neither CTA leaves while the other's MMAs or loads use it
@@ -491,9 +651,9 @@ int resident_pairs(K k, size_t smem, int* cache) {
   return cache[dev];
 }
 
-template <bool kNv, int kBN, bool kPair, bool kBf16>
+template <bool kNv, int kBN, int kOut>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  using Sh = Shape<kNv, kBN, kPair>;
+  using Sh = Shape<kNv, kBN, kOut>;
   static int smem_set[64], pairs[64];
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
@@ -507,12 +667,12 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s)
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks * a.G;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
-  auto k = fp4_linear_kernel<kNv, kBN, kPair, kBf16>;
+  auto k = fp4_linear_kernel<kNv, kBN, kOut>;
   const cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(k), Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const dim3 block(kThreads);
   p.splits = 1;
-  if constexpr (kPair) {
+  if constexpr (Sh::kPair) {
     const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
     return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, p);
   } else {
@@ -526,16 +686,15 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s)
   }
 }
 
-template <bool kNv, bool kBf16>
+template <bool kNv, int kOut>
 cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  // tokens per tile: the smallest that takes them all; beyond 128, pairs of CTAs once there is a
-  // tile for every second pair, else lone 256-token tiles whose K axis can be split
-  if (a.M <= 32) return launch_tile<kNv, 32, false, kBf16>(a, p, s);
-  if (a.M <= 64) return launch_tile<kNv, 64, false, kBf16>(a, p, s);
-  if (a.M <= 128) return launch_tile<kNv, 128, false, kBf16>(a, p, s);
+  // tokens per tile: the smallest of 32, 64 and 128 that takes them all; beyond 128, pairs of CTAs
+  // once there is a tile for every second pair, else lone 128-token tiles whose K axis can be split
   const int64_t pairs = (static_cast<int64_t>(a.N) + 255) / 256 * ((a.M + 255) / 256) * a.G;
-  if (4 * pairs >= num_sms()) return launch_tile<kNv, 256, true, kBf16>(a, p, s);
-  return launch_tile<kNv, 256, false, kBf16>(a, p, s);
+  if (a.M > 128 && 4 * pairs >= num_sms()) return launch_tile<kNv, 256, kOut>(a, p, s);
+  if (a.M <= 32) return launch_tile<kNv, 32, kOut>(a, p, s);
+  if (a.M <= 64) return launch_tile<kNv, 64, kOut>(a, p, s);
+  return launch_tile<kNv, 128, kOut>(a, p, s);
 }
 
 }  // namespace
@@ -556,18 +715,23 @@ cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s) {
   p.ldy = a.ldy;
   p.vec2 = a.N % 2 == 0 && a.ldy % 2 == 0;
   p.vec4 = a.N % 4 == 0 && a.ldy % 4 == 0;
+  p.z_packed = a.z_packed;
+  p.z_scale = a.z_scale;
+  p.gz = a.gz;
+  p.z_atoms = fp4_atoms(a.nv, a.G * a.N);
   p.err = device_error_word();
   if (p.err == nullptr) return cudaErrorUnknown;
-  if (a.nv) return a.out_bf16 ? launch_shape<true, true>(a, p, s) : launch_shape<true, false>(a, p, s);
-  return a.out_bf16 ? launch_shape<false, true>(a, p, s) : launch_shape<false, false>(a, p, s);
+  if (a.z_packed != nullptr) return a.nv ? launch_shape<true, kOutFp4>(a, p, s) : launch_shape<false, kOutFp4>(a, p, s);
+  if (a.nv) return a.out_bf16 ? launch_shape<true, kOutBf16>(a, p, s) : launch_shape<true, kOutF32>(a, p, s);
+  return a.out_bf16 ? launch_shape<false, kOutBf16>(a, p, s) : launch_shape<false, kOutF32>(a, p, s);
 }
 
 // ------------------------------------------------------------------ grouped output projection
-// Scratch of the projection, 256-byte aligned pieces: o's codes and scales, z (bf16), z's
-// codes and scales.
+// Scratch of the projection, 256-byte aligned pieces: the codes and scales of o and of z (the
+// first product encodes z as it writes it).
 namespace {
 struct ProjScratch {
-  size_t o_packed, o_scale, z, z_packed, z_scale, bytes;
+  size_t o_packed, o_scale, z_packed, z_scale, bytes;
 };
 ProjScratch proj_scratch(bool nv, int T, int64_t HD, int64_t GR) {
   ProjScratch w{};
@@ -579,7 +743,6 @@ ProjScratch proj_scratch(bool nv, int T, int64_t HD, int64_t GR) {
   };
   w.o_packed = take(static_cast<size_t>(T) * HD / 2);
   w.o_scale = take(fp4_scale_bytes(nv, T, static_cast<int>(HD)));
-  w.z = take(static_cast<size_t>(T) * GR * 2);
   w.z_packed = take(static_cast<size_t>(T) * GR / 2);
   w.z_scale = take(fp4_scale_bytes(nv, T, static_cast<int>(GR)));
   w.bytes = at;
@@ -608,13 +771,13 @@ cudaError_t launch_grouped_out_proj_fp4(const Fp4ProjArgs& a, cudaStream_t s) {
   l.w_packed = a.a_packed;
   l.w_scale = a.a_scale;
   l.gw = a.ga;
-  l.out_bf16 = 1;
-  l.y = ws + w.z;
-  l.ldy = GR;
+  l.z_packed = ws + w.z_packed;
+  l.z_scale = ws + w.z_scale;
+  l.gz = a.gz;
   e = launch_fp4_linear(l, s);
   if (e != cudaSuccess) return e;
-  e = launch_fp4_quantize(a.nv, ws + w.z, 1, a.T, GR, GR, a.gz, ws + w.z_packed, ws + w.z_scale, s);
-  if (e != cudaSuccess) return e;
+  l.z_packed = l.z_scale = nullptr;
+  l.out_bf16 = 1;
   l.N = a.d_model;
   l.K = GR;
   l.G = 1;

@@ -133,6 +133,9 @@ struct Fp4LinearArgs {
   int out_bf16;
   void* y;                  // [M, ldy]
   int64_t ldy;
+  uint8_t* z_packed;        // non-null: the result is rounded to bf16 and encoded instead (N a
+  uint8_t* z_scale;         // multiple of 128): codes [M, G N / 2], scales, tensor scale
+  const float* gz;
 };
 cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s);
 

@@ -168,7 +168,8 @@ def test_linear_into_a_wider_tensor(B, cuda, fmt, M):
     assert torch.equal(wide[:, :136], B.csa_fp4_linear(mx, mw)) and (wide[:, 136:] == 3).all()
 
 
-PROJ_SHAPES = [(1, 16, 128, 4, 256, 512), (37, 16, 128, 4, 256, 512), (200, 8, 64, 2, 128, 130), (300, 4, 32, 1, 384, 77)]
+PROJ_SHAPES = [(1, 16, 128, 4, 256, 512), (37, 16, 128, 4, 256, 512), (200, 8, 64, 2, 128, 130), (300, 4, 32, 1, 384, 77),
+               (1500, 16, 64, 8, 128, 1300), (2100, 8, 64, 2, 640, 96)]  # the last two: pairs of CTAs encode z
 
 
 @pytest.mark.parametrize("fmt", FMTS)
