@@ -9,13 +9,15 @@
 //
 // Scales are stored as the tensor core reads them: blocks of 128 rows x 4 scales, 512 bytes,
 // the scale (r, b) of a block at byte (r % 32) * 16 + (r / 32) * 4 + b; row blocks outermost.
-// So one warp takes the four rows r, r + 32, r + 64, r + 96 of a row block over 256 columns:
-// the four rows' scales of an atom are 16 consecutive bytes, and four loads are in flight per
-// lane.  Rows and columns that pad a block get scale bytes of zero.
+// So one warp takes the four rows r, r + 32, r + 64, r + 96 of a row block over its columns:
+// the four rows' scales of an atom are 16 consecutive bytes, and the loads of all four are in
+// flight before the first is used.  Rows and columns that pad a block get scale bytes of zero.
 //
 // All three kernels are bound by HBM: 2 or 4 bytes read and 17/32 or 9/16 written per element.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -25,15 +27,90 @@ namespace csa {
 namespace {
 
 constexpr int kFp4Threads = 256;
-constexpr int kChunk = 256;  // columns of a warp's task: 8 per lane
 
 struct Fp4Shape {
   int64_t rows;
   int cols;
   int64_t ld;      // elements between rows of the unencoded matrix
   int n_atoms;     // scale atoms (4 scales) per row
-  int n_chunks;    // ceil(padded columns / 256)
-  int64_t n_tasks; // row blocks * 32 * n_chunks
+  int n_chunks;    // columns in units of a warp's task
+  int64_t n_rows32; // row blocks * 32
+};
+
+// A warp's tasks: (row, chunk) pairs, chunks fastest, `n_warps` apart -- stepped without a division
+struct Task {
+  int64_t row, step_row;
+  int chunk, step_chunk;
+  __device__ Task(int64_t warp, int64_t n_warps, int n_chunks)
+      : row(warp / n_chunks), step_row(n_warps / n_chunks), chunk(static_cast<int>(warp % n_chunks)),
+        step_chunk(static_cast<int>(n_warps % n_chunks)) {}
+  __device__ void next(int n_chunks) {
+    row += step_row;
+    chunk += step_chunk;
+    if (chunk >= n_chunks) {
+      chunk -= n_chunks;
+      ++row;
+    }
+  }
+};
+
+// What a lane encodes of one row: 32 bytes, 16 bf16 or 8 float32 (half or a quarter of an MXFP4
+// block, a whole NVFP4 block or half of one).
+template <bool kBf16>
+constexpr int kEncodePer = kBf16 ? 16 : 8;
+template <bool kBf16>
+constexpr int kEncodeChunk = 32 * kEncodePer<kBf16>;  // columns of a warp's task
+
+template <bool kBf16, bool kNv>
+struct RowTask {
+  static constexpr int kPer = kEncodePer<kBf16>, kUnits = kPer / 8, kBlk = kNv ? 16 : 32;
+  static constexpr int kBlkLanes = kBlk / kPer, kAtomLanes = 4 * kBlkLanes;
+  Raw8<kBf16> raw[kUnits];
+
+  __device__ __forceinline__ void load(const void* x, int64_t at, bool in) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      if (in)
+        raw[u].load(x, at + 8 * u);
+      else
+        raw[u].zero();
+    }
+  }
+  // stores the codes (where `in`) and returns the atom's four scale bytes, in each of its lanes
+  __device__ __forceinline__ uint32_t encode(float g, float six_g, uint8_t* packed, int64_t at, bool in) const {
+    const int lane = threadIdx.x & 31;
+    float am = raw[0].amax();
+#pragma unroll
+    for (int u = 1; u < kUnits; ++u) am = fmaxf(am, raw[u].amax());
+#pragma unroll
+    for (int o = 1; o < kBlkLanes; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    uint32_t byte, word[kUnits];
+    float T = 0.f;
+    if constexpr (kNv) {
+      byte = nv_scale_byte(am, six_g);
+      T = e4m3_value(byte) * g;
+    } else {
+      const int E = mx_block_exponent(am);
+      T = mx_pow2_neg(E);
+      byte = static_cast<uint32_t>(E + 127);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      float v[8];
+      raw[u].values(v);
+      word[u] = kNv ? nv_codes8(v, T, am) : e2m1x8_rn(v, T);
+    }
+    if (in) {
+      if constexpr (kUnits == 2)
+        *reinterpret_cast<uint2*>(packed + at / 2) = make_uint2(word[0], word[1]);
+      else
+        *reinterpret_cast<uint32_t*>(packed + at / 2) = word[0];
+    }
+    uint32_t w = in ? byte << (8 * ((lane / kBlkLanes) & 3)) : 0u;
+    w |= __shfl_xor_sync(0xffffffffu, w, kBlkLanes);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2 * kBlkLanes);
+    return w;
+  }
 };
 
 template <bool kBf16, bool kNv>
@@ -41,63 +118,48 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
                                                                    const float* __restrict__ tensor_scale,
                                                                    uint8_t* __restrict__ packed,
                                                                    uint8_t* __restrict__ scales) {
+  using RT = RowTask<kBf16, kNv>;
   griddep_enter();
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kFp4Threads + threadIdx.x) >> 5;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kFp4Threads / 32);
   const float g = kNv ? __ldg(tensor_scale) : 1.f;
   const float six_g = 6.f * g;
-  for (int64_t task = warp0; task < p.n_tasks; task += n_warps) {
-    const int chunk = static_cast<int>(task % p.n_chunks);
-    const int64_t rest = task / p.n_chunks;
-    const int r32 = static_cast<int>(rest & 31);
-    const int64_t rb = rest >> 5;
-    const int col = chunk * kChunk + lane * 8;
-    float v[4][8];
+  for (Task t(warp0, n_warps, p.n_chunks); t.row < p.n_rows32; t.next(p.n_chunks)) {
+    const int r32 = t.row & 31;
+    const int64_t row0 = (t.row >> 5) * 128 + r32;
+    const int col = t.chunk * kEncodeChunk<kBf16> + lane * RT::kPer;
+    const bool in = col < p.cols;  // cols is a multiple of 32: a lane's columns are all in or all out
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (row0 + 96 < p.rows) {
+      RT rt[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = rb * 128 + r32 + 32 * i;
-      if (row < p.rows && col < p.cols) {  // cols is a multiple of 32: a lane's 8 are all in or all out
-        fp4_load8<kBf16>(x, row * p.ld + col, v[i]);
-      } else {
+      for (int i = 0; i < 4; ++i) rt[i].load(x, (row0 + 32 * i) * p.ld + col, in);  // every load first
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(g, six_g, packed, (row0 + 32 * i) * p.cols + col, in);
+    } else {  // the last row block: one row at a time, so that rows that only pad it cost nothing
+#pragma unroll 1
+      for (int64_t row = row0; row < p.rows; row += 32) {
+        RT rt;
+        rt.load(x, row * p.ld + col, in);
+        const uint32_t v = rt.encode(g, six_g, packed, row * p.cols + col, in);
+        const int i = static_cast<int>((row - row0) / 32);
+        w[0] = i == 0 ? v : w[0];
+        w[1] = i == 1 ? v : w[1];
+        w[2] = i == 2 ? v : w[2];
       }
     }
-    uint32_t sword[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = rb * 128 + r32 + 32 * i;
-      const bool in = row < p.rows && col < p.cols;
-      float am = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(v[i][e]));
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      uint32_t word, byte;
-      if constexpr (kNv) {
-        byte = nv_scale_byte(am, six_g);
-        word = nv_codes8(v[i], e4m3_value(byte) * g);
-      } else {
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        const int E = mx_block_exponent(am);
-        word = e2m1x8_rn(v[i], mx_pow2_neg(E));
-        byte = static_cast<uint32_t>(E + 127);
-      }
-      if (in) reinterpret_cast<uint32_t*>(packed)[(row * p.cols + col) >> 3] = word;
-      // the four scale bytes of an atom (16 lanes; NVFP4: 8) into one word, in every lane
-      constexpr int kStep = kNv ? 2 : 4;  // lanes per block
-      uint32_t w = in ? byte << (8 * ((lane / kStep) & 3)) : 0u;
-      w |= __shfl_xor_sync(0xffffffffu, w, kStep);
-      w |= __shfl_xor_sync(0xffffffffu, w, 2 * kStep);
-      sword[i] = w;
-    }
-    constexpr int kLanes = kNv ? 8 : 16;  // lanes per atom
-    const int atom = chunk * (32 / kLanes) + lane / kLanes;
-    if (lane % kLanes == 0 && atom < p.n_atoms)
-      *reinterpret_cast<uint4*>(scales + fp4_atom_offset(rb, atom, p.n_atoms) + r32 * 16) =
-          make_uint4(sword[0], sword[1], sword[2], sword[3]);
+    const int atom = (t.chunk * 32 + lane) / RT::kAtomLanes;
+    if (lane % RT::kAtomLanes == 0 && atom < p.n_atoms)
+      *reinterpret_cast<uint4*>(scales + fp4_atom_offset(t.row >> 5, atom, p.n_atoms) + r32 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
+
+// Decoding writes 2 or 4 bytes for every half byte read, so the mapping follows the stores: a lane
+// takes 16 bytes of output at a time (8 bf16 or 4 float32), twice per row, each warp store
+// contiguous.
+template <bool kBf16>
+constexpr int kDecodeChunk = kBf16 ? 512 : 256;  // columns of a warp's task
 
 template <bool kBf16, bool kNv>
 __global__ void __launch_bounds__(kFp4Threads) fp4_dequantize_kernel(const uint8_t* __restrict__ packed,
@@ -109,35 +171,48 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_dequantize_kernel(const uint8
   const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kFp4Threads + threadIdx.x) >> 5;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kFp4Threads / 32);
   const float g = kNv ? __ldg(tensor_scale) : 1.f;
-  constexpr int kLanes = kNv ? 8 : 16;
-  constexpr int kStep = kNv ? 2 : 4;
-  for (int64_t task = warp0; task < p.n_tasks; task += n_warps) {
-    const int chunk = static_cast<int>(task % p.n_chunks);
-    const int64_t rest = task / p.n_chunks;
-    const int r32 = static_cast<int>(rest & 31);
-    const int64_t rb = rest >> 5;
-    const int col = chunk * kChunk + lane * 8;
-    if (rb * 128 + r32 >= p.rows || col >= p.cols) continue;  // no shuffles below: lanes may part
-    const int atom = chunk * (32 / kLanes) + lane / kLanes;
-    const uint4 sv = __ldg(reinterpret_cast<const uint4*>(scales + fp4_atom_offset(rb, atom, p.n_atoms) + r32 * 16));
-    const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
-    uint32_t word[4];
+  constexpr int kPer = kBf16 ? 8 : 4, kBlk = kNv ? 16 : 32;
+  using Codes = typename std::conditional<kBf16, uint32_t, uint16_t>::type;
+  for (Task t(warp0, n_warps, p.n_chunks); t.row < p.n_rows32; t.next(p.n_chunks)) {
+    const int r32 = t.row & 31;
+    const int64_t rb = t.row >> 5;
+    if (rb * 128 + r32 >= p.rows) continue;
+    uint4 sv[2];
+    Codes word[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = rb * 128 + r32 + 32 * i;
-      word[i] = row < p.rows ? __ldg(reinterpret_cast<const uint32_t*>(packed) + ((row * p.cols + col) >> 3)) : 0u;
+    for (int h = 0; h < 2; ++h) {  // every load first
+      const int col = t.chunk * kDecodeChunk<kBf16> + (h * 32 + lane) * kPer;
+      if (col < p.cols)
+        sv[h] = __ldg(reinterpret_cast<const uint4*>(scales + fp4_atom_offset(rb, col / (4 * kBlk), p.n_atoms) + r32 * 16));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = rb * 128 + r32 + 32 * i;
+        word[h][i] = row < p.rows && col < p.cols
+                         ? __ldg(reinterpret_cast<const Codes*>(packed) + (row * p.cols + col) / kPer)
+                         : static_cast<Codes>(0);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = rb * 128 + r32 + 32 * i;
-      if (row >= p.rows) break;
-      const uint32_t byte = (sw[i] >> (8 * ((lane / kStep) & 3))) & 0xFFu;
-      const float T = kNv ? e4m3_value(byte) * g : ue8m0_value(byte);
-      float v[8];
-      e2m1x8_values(word[i], v);
+    for (int h = 0; h < 2; ++h) {
+      const int col = t.chunk * kDecodeChunk<kBf16> + (h * 32 + lane) * kPer;
+      if (col >= p.cols) continue;
+      const uint32_t sw[4] = {sv[h].x, sv[h].y, sv[h].z, sv[h].w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= T;
-      fp4_store8<kBf16>(out, row * p.ld + col, v);
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = rb * 128 + r32 + 32 * i;
+        if (row >= p.rows) break;
+        const uint32_t byte = (sw[i] >> (8 * (col / kBlk & 3))) & 0xFFu;
+        const float T = kNv ? e4m3_value(byte) * g : ue8m0_value(byte);
+        float v[kPer];
+        e2m1_values<kPer>(word[h][i], v);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] *= T;
+        if constexpr (kBf16)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * p.ld + col) =
+              make_uint4(fp4_bf16x2(v[0], v[1]), fp4_bf16x2(v[2], v[3]), fp4_bf16x2(v[4], v[5]), fp4_bf16x2(v[6], v[7]));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(out) + row * p.ld + col) = make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
   }
 }
@@ -164,14 +239,14 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_pack_scales_kernel(const uint
   }
 }
 
-Fp4Shape fp4_shape(bool nv, int64_t rows, int cols, int64_t ld) {
+Fp4Shape fp4_shape(bool nv, int64_t rows, int cols, int64_t ld, int chunk) {
   Fp4Shape p{};
   p.rows = rows;
   p.cols = cols;
   p.ld = ld;
   p.n_atoms = fp4_atoms(nv, cols);
-  p.n_chunks = (cols + kChunk - 1) / kChunk;
-  p.n_tasks = (rows + 127) / 128 * 32 * p.n_chunks;
+  p.n_chunks = (cols + chunk - 1) / chunk;
+  p.n_rows32 = (rows + 127) / 128 * 32;
   return p;
 }
 
@@ -191,8 +266,8 @@ size_t fp4_scale_bytes(bool nv, int64_t rows, int cols) {
 cudaError_t launch_fp4_quantize(bool nv, const void* x, int in_bf16, int64_t rows, int cols, int64_t ld,
                                 const float* tensor_scale, uint8_t* packed, uint8_t* scales, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
-  const Fp4Shape p = fp4_shape(nv, rows, cols, ld);
-  const dim3 grid(fp4_grid(p.n_tasks)), block(kFp4Threads);
+  const Fp4Shape p = fp4_shape(nv, rows, cols, ld, in_bf16 ? kEncodeChunk<true> : kEncodeChunk<false>);
+  const dim3 grid(fp4_grid(p.n_rows32 * p.n_chunks)), block(kFp4Threads);
   auto k = nv ? (in_bf16 ? fp4_quantize_kernel<true, true> : fp4_quantize_kernel<false, true>)
               : (in_bf16 ? fp4_quantize_kernel<true, false> : fp4_quantize_kernel<false, false>);
   return launch_pdl(k, grid, block, 0, s, x, p, tensor_scale, packed, scales);
@@ -201,8 +276,8 @@ cudaError_t launch_fp4_quantize(bool nv, const void* x, int in_bf16, int64_t row
 cudaError_t launch_fp4_dequantize(bool nv, const uint8_t* packed, const uint8_t* scales, const float* tensor_scale,
                                   int64_t rows, int cols, int out_bf16, void* out, int64_t ld, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
-  const Fp4Shape p = fp4_shape(nv, rows, cols, ld);
-  const dim3 grid(fp4_grid(p.n_tasks)), block(kFp4Threads);
+  const Fp4Shape p = fp4_shape(nv, rows, cols, ld, out_bf16 ? kDecodeChunk<true> : kDecodeChunk<false>);
+  const dim3 grid(fp4_grid(p.n_rows32 * p.n_chunks)), block(kFp4Threads);
   auto k = nv ? (out_bf16 ? fp4_dequantize_kernel<true, true> : fp4_dequantize_kernel<false, true>)
               : (out_bf16 ? fp4_dequantize_kernel<true, false> : fp4_dequantize_kernel<false, false>);
   return launch_pdl(k, grid, block, 0, s, packed, scales, p, tensor_scale, out);

@@ -32,11 +32,39 @@ __device__ __forceinline__ uint32_t nv_scale_byte(float amax, float six_g) {
   return __nv_cvt_float_to_fp8(__fdiv_rn(amax, six_g), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Codes of eight values under the NVFP4 scale T: e2m1(x / T), zeros if T is zero
-__device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T) {
+// x / T correctly rounded, given r = 1 / T correctly rounded, for |x| <= 8 T and T in
+// [2^-90, 2^100]: two residual steps (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990).  q0 is within 1.5 units in the last place, q1 within one,
+// and a residual step from a quotient within one unit, with a correctly rounded reciprocal, rounds
+// correctly.  Residuals of an x too small for an exact one only meet quotients that encode as 0.
+// The residual is taken as q T - x, so that a zero keeps its sign.
+__device__ __forceinline__ float div_given_rcp(float x, float T, float r) {
+  const float q0 = x * r;
+  const float q1 = fmaf(-fmaf(q0, T, -x), r, q0);
+  return fmaf(-fmaf(q1, T, -x), r, q1);
+}
+
+// the same by plain division (out of line: eight of them would crowd the instruction cache of
+// every kernel that encodes, and only blocks with an extreme scale come here)
+static __device__ __noinline__ uint32_t nv_codes8_div(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
+                                               float v7, float T) {
+  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = T > 0.f ? __fdiv_rn(v[i], T) : 0.f;
+  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(v[i], T);
+  return e2m1x8_rn(y, 1.f);
+}
+
+// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T), zeros if T is zero.
+// amax: the block's; where its scale is cut at 448 or T is extreme, plain division.
+__device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T, float amax) {
+  if (T == 0.f) return 0u;
+  if (!(T >= 0x1p-90f && T <= 0x1p100f && amax <= 8.f * T))
+    return nv_codes8_div(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], T);
+  const float r = __frcp_rn(T);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = div_given_rcp(v[i], T, r);
   return e2m1x8_rn(y, 1.f);
 }
 
@@ -45,10 +73,11 @@ __device__ __forceinline__ float ue8m0_value(uint32_t byte) {
   return byte == 255u ? __uint_as_float(0x7FC00000u) : (byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23));
 }
 
-// the values of eight packed codes (the even element in the low nibble); exact in f16
-__device__ __forceinline__ void e2m1x8_values(uint32_t word, float (&v)[8]) {
+// the values of kN packed codes (the even element in the low nibble); exact in f16
+template <int kN>
+__device__ __forceinline__ void e2m1_values(uint32_t word, float (&v)[kN]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kN / 2; ++i) {
     uint32_t h;
     asm("{\n\t.reg .b8 q;\n\t"
         "cvt.u8.u32 q, %1;\n\t"
@@ -61,45 +90,62 @@ __device__ __forceinline__ void e2m1x8_values(uint32_t word, float (&v)[8]) {
   }
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void fp4_load8(const void* x, int64_t at, float (&v)[8]) {
-  if constexpr (kBf16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-}
-
-__device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // larger of two pairs of bf16, NaNs left out
 __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+// largest magnitude of eight bf16, NaNs left out (0 if there is nothing else)
+__device__ __forceinline__ float bf16x8_amax(const uint4& u) {
+  const uint32_t a = bf16x2_max(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), b = bf16x2_max(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu);
+  const uint32_t m = bf16x2_max(a, b);
+  return fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), 0.f);
+}
+
+// eight values as they lie in memory (16 bytes of bf16, 32 of float32), and as floats
 template <bool kBf16>
-__device__ __forceinline__ void fp4_store8(void* out, int64_t at, const float (&v)[8]) {
-  if constexpr (kBf16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
-        make_uint4(fp4_bf16x2(v[0], v[1]), fp4_bf16x2(v[2], v[3]), fp4_bf16x2(v[4], v[5]), fp4_bf16x2(v[6], v[7]));
-  } else {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+struct Raw8;
+template <>
+struct Raw8<true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
   }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float amax() const { return bf16x8_amax(u); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Raw8<false> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* x, int64_t at) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    a = __ldg(s);
+    b = __ldg(s + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float amax() const {
+    const float m0 = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+    const float m1 = fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w)));
+    return fmaxf(fmaxf(m0, m1), 0.f);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ uint32_t fp4_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
 }
 
 }  // namespace csa

@@ -129,23 +129,23 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
   const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
   uint32_t codes[4], bytes = 0;
-  float inv[2];
+  float inv[2], top[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // halves of 16: a block each (NVFP4) or together (MXFP4)
     uint32_t am = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) am = bf16x2_max(am, w[8 * h + i] & 0x7FFF7FFFu);
-    inv[h] = fmaxf(__uint_as_float(am << 16), __uint_as_float(am & 0xFFFF0000u));
+    top[h] = fmaxf(fmaxf(__uint_as_float(am << 16), __uint_as_float(am & 0xFFFF0000u)), 0.f);
   }
   if constexpr (kNv) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t byte = nv_scale_byte(inv[h], 6.f * g);
+      const uint32_t byte = nv_scale_byte(top[h], 6.f * g);
       bytes |= byte << (8 * h);
       inv[h] = e4m3_value(byte) * g;  // T
     }
   } else {
-    const int E = mx_block_exponent(fmaxf(inv[0], inv[1]));
+    const int E = mx_block_exponent(fmaxf(top[0], top[1]));
     bytes = E + 127;
     inv[0] = inv[1] = mx_pow2_neg(E);
   }
@@ -157,7 +157,7 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
       v[2 * i] = __uint_as_float(w[4 * q + i] << 16);
       v[2 * i + 1] = __uint_as_float(w[4 * q + i] & 0xFFFF0000u);
     }
-    codes[q] = kNv ? nv_codes8(v, inv[q / 2]) : e2m1x8_rn(v, inv[q / 2]);
+    codes[q] = kNv ? nv_codes8(v, inv[q / 2], top[q / 2]) : e2m1x8_rn(v, inv[q / 2]);
   }
   const int lane = threadIdx.x & 31;
   if constexpr (kNv) {  // two bytes per lane: lanes 0, 1 hold one atom's four scales, lanes 2, 3 the next's

@@ -62,9 +62,16 @@ __device__ __forceinline__ uint32_t e2m1x2_rn(float lo, float hi) {
 // Eight values scaled by inv_T = 2^-E into four packed bytes (element 2i in the low nibble
 // of byte i).
 __device__ __forceinline__ uint32_t e2m1x8_rn(const float (&v)[8], float inv_T) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= e2m1x2_rn(v[2 * i] * inv_T, v[2 * i + 1] * inv_T) << (8 * i);
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
+      : "=r"(w)
+      : "f"(v[0] * inv_T), "f"(v[1] * inv_T), "f"(v[2] * inv_T), "f"(v[3] * inv_T), "f"(v[4] * inv_T),
+        "f"(v[5] * inv_T), "f"(v[6] * inv_T), "f"(v[7] * inv_T));
   return w;
 }
 
