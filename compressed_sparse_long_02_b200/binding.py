@@ -448,6 +448,18 @@ def _tensor_scale(fmt: str, g: torch.Tensor | None, dev, name="tensor_scale"):
 
 def _fp4_mat(m: Fp4Matrix, name: str, dev) -> _Fp4Mat:
     fmt, rows, cols, packed, scales, g = m
+    if (fmt not in _FP4_FMT or rows < 0 or cols < 32 or cols % 32 or packed.dtype is not torch.uint8
+            or scales.dtype is not torch.uint8 or packed.device != dev or scales.device != dev
+            or not packed.is_contiguous() or not scales.is_contiguous() or packed.numel() != rows * (cols // 2)
+            or scales.numel() < _scale_bytes(fmt, rows, cols)):
+        _refuse_mat(m, name, dev)
+    return _Fp4Mat(packed.data_ptr(), scales.data_ptr(), g if g is None and fmt == "mxfp4" else
+                   _tensor_scale(fmt, g, dev, f"{name}.tensor_scale"))
+
+
+def _refuse_mat(m: Fp4Matrix, name: str, dev):
+    """Raises for the first thing that is wrong with m."""
+    fmt, rows, cols, packed, scales, _ = m
     _fmt(fmt)
     if rows < 0 or cols < 32 or cols % 32:
         raise ValueError(f"{name}: cols must be a positive multiple of 32, got {cols}")
@@ -458,9 +470,7 @@ def _fp4_mat(m: Fp4Matrix, name: str, dev) -> _Fp4Mat:
             raise ValueError(f"{name}.{nm} must be contiguous on {dev}")
     if packed.numel() != rows * (cols // 2):
         raise ValueError(f"{name}.packed must hold {rows} x {cols // 2} bytes, got {packed.numel()}")
-    if scales.numel() < _scale_bytes(fmt, rows, cols):
-        raise ValueError(f"{name}.scales is smaller than csa_fp4_scale_bytes({fmt}, {rows}, {cols})")
-    return _Fp4Mat(packed.data_ptr(), scales.data_ptr(), _tensor_scale(fmt, g, dev, f"{name}.tensor_scale"))
+    raise ValueError(f"{name}.scales is smaller than csa_fp4_scale_bytes({fmt}, {rows}, {cols})")
 
 
 def _rows_2d(t: torch.Tensor, name: str):
@@ -485,11 +495,14 @@ def _rows_2d(t: torch.Tensor, name: str):
     return rows, cols, ld
 
 
+_here = contextlib.nullcontext()
+
+
 def _on(t: torch.Tensor):
     """The device guard of a call on t's device (nothing when it is the current one)."""
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _here if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
 def csa_fp4_scale_bytes(fmt: str, rows: int, cols: int) -> int:
@@ -506,17 +519,24 @@ def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch
         raise ValueError(f"x's last dimension must be a positive multiple of 32, got {cols}")
     if out is None:
         # one allocation: the codes, then the scales from the next multiple of 256 bytes
-        n, at = rows * (cols // 2), (rows * (cols // 2) + 255) // 256 * 256
-        buf = torch.empty(at + _scale_bytes(fmt, rows, cols), dtype=torch.uint8, device=dev)
-        out = Fp4Matrix(fmt, rows, cols, buf[:n].view(rows, cols // 2), buf[at:], tensor_scale)
-    elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
-        raise ValueError(f"out must be a {fmt} matrix of {rows} x {cols}")
-    elif out.tensor_scale is not tensor_scale:
-        out = out._replace(tensor_scale=tensor_scale)
-    with _on(x):
+        n = rows * (cols // 2)
+        at = (n + 255) // 256 * 256
+        ns = _scale_bytes(fmt, rows, cols)
+        buf = torch.empty(at + ns, dtype=torch.uint8, device=dev)
+        packed, scales = buf.as_strided((rows, cols // 2), (cols // 2, 1)), buf.as_strided((ns,), (1,), at)
+        out = Fp4Matrix(fmt, rows, cols, packed, scales, tensor_scale)
+        base = buf.data_ptr()
+        m = _Fp4Mat(base, base + at, _tensor_scale(fmt, tensor_scale, dev))
+    else:
+        if (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
+            raise ValueError(f"out must be a {fmt} matrix of {rows} x {cols}")
+        if out.tensor_scale is not tensor_scale:
+            out = out._replace(tensor_scale=tensor_scale)
         m = _fp4_mat(out, "out", dev)
+    with _on(x):
         st = lib().csa_fp4_quantize(f, x.data_ptr(), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
-    _check("csa_fp4_quantize", st)
+    if st:
+        _check("csa_fp4_quantize", st)
     return out
 
 
@@ -524,7 +544,7 @@ def csa_fp4_dequantize(m: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat16, out
     """The values of m, [rows, cols] in dtype (float32 or bf16), or into `out` (evenly spaced rows)."""
     dev = m.packed.device
     if out is None:
-        out = torch.empty((m.rows, m.cols), dtype=dtype, device=dev)
+        out = m.packed.new_empty((m.rows, m.cols), dtype=dtype)
     dt = _dt(out)
     rows, cols, ld = _rows_2d(out, "out")
     if rows != m.rows or cols != m.cols or out.device != dev:
@@ -532,7 +552,8 @@ def csa_fp4_dequantize(m: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat16, out
     with _on(out):
         c = _fp4_mat(m, "m", dev)
         st = lib().csa_fp4_dequantize(_FP4_FMT[m.fmt], ctypes.byref(c), rows, cols, dt, out.data_ptr(), ld, _stream(out))
-    _check("csa_fp4_dequantize", st)
+    if st:
+        _check("csa_fp4_dequantize", st)
     return out
 
 
@@ -559,7 +580,7 @@ def csa_fp4_linear(x: Fp4Matrix, w: Fp4Matrix, *, groups: int = 1, out_dtype: to
     if G < 1 or w.rows % G or x.cols != G * K:
         raise ValueError(f"x {x.rows} x {x.cols} and w {w.rows} x {w.cols} do not fit {G} groups")
     if out is None:
-        out = torch.empty((M, w.rows), dtype=out_dtype, device=dev)
+        out = x.packed.new_empty((M, w.rows), dtype=out_dtype)
     dt = _dt(out)
     rows, cols, ld = _rows_2d(out, "out")
     if rows != M or cols != w.rows or out.device != dev:
@@ -568,7 +589,8 @@ def csa_fp4_linear(x: Fp4Matrix, w: Fp4Matrix, *, groups: int = 1, out_dtype: to
         cx, cw = _fp4_mat(x, "x", dev), _fp4_mat(w, "w", dev)
         st = lib().csa_fp4_linear(_FP4_FMT[fmt], M, w.rows // G, K, G, ctypes.byref(cx), ctypes.byref(cw), dt,
                                   out.data_ptr(), ld, _stream(out))
-    _check("csa_fp4_linear", st)
+    if st:
+        _check("csa_fp4_linear", st)
     return out
 
 
@@ -590,11 +612,11 @@ def csa_grouped_out_proj_fp4(o: torch.Tensor, A: Fp4Matrix, Bm: Fp4Matrix, *, gr
         raise ValueError("inconsistent projection shapes")
     R, d_model = A.rows // G, Bm.rows
     if out is None:
-        out = torch.empty((T, d_model), dtype=torch.bfloat16, device=dev)
+        out = o.new_empty((T, d_model))
     else:
         _need(out, torch.bfloat16, (T, d_model), "out")
     if workspace is None:
-        workspace = torch.empty(csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R), dtype=torch.uint8, device=dev)
+        workspace = o.new_empty(csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R), dtype=torch.uint8)
     if out.device != dev or workspace.device != dev:
         raise ValueError(f"out and workspace must be on {dev}")
     with _on(o):
@@ -603,7 +625,8 @@ def csa_grouped_out_proj_fp4(o: torch.Tensor, A: Fp4Matrix, Bm: Fp4Matrix, *, gr
                                             _tensor_scale(fmt, o_scale, dev, "o_scale"), ctypes.byref(ca),
                                             _tensor_scale(fmt, z_scale, dev, "z_scale"), ctypes.byref(cb), _ptr(out),
                                             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(o))
-    _check("csa_grouped_out_proj_fp4", st)
+    if st:
+        _check("csa_grouped_out_proj_fp4", st)
     return out
 
 

@@ -44,27 +44,38 @@ __device__ __forceinline__ float div_given_rcp(float x, float T, float r) {
   return fmaf(-fmaf(q1, T, -x), r, q1);
 }
 
-// the same by plain division (out of line: eight of them would crowd the instruction cache of
-// every kernel that encodes, and only blocks with an extreme scale come here)
-static __device__ __noinline__ uint32_t nv_codes8_div(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
-                                               float v7, float T) {
-  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(v[i], T);
-  return e2m1x8_rn(y, 1.f);
+// four quotients by plain division (out of line: unrolled, they would crowd the instruction cache
+// of every kernel that encodes, and only blocks with an extreme scale come here)
+static __device__ __noinline__ float4 div4(float a, float b, float c, float d, float T) {
+  return make_float4(__fdiv_rn(a, T), __fdiv_rn(b, T), __fdiv_rn(c, T), __fdiv_rn(d, T));
 }
 
-// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T), zeros if T is zero.
+// The quotients x / T of kN values of a block under its NVFP4 scale T (zeros if T is zero).
 // amax: the block's; where its scale is cut at 448 or T is extreme, plain division.
+template <int kN>
+__device__ __forceinline__ void nv_quotients(float (&v)[kN], float T, float amax) {
+  if (T == 0.f) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = 0.f;
+  } else if (!(T >= 0x1p-90f && T <= 0x1p100f && amax <= 8.f * T)) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+      const float4 q = div4(v[i], v[i + 1], v[i + 2], v[i + 3], T);
+      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    }
+  } else {
+    const float r = __frcp_rn(T);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = div_given_rcp(v[i], T, r);
+  }
+}
+
+// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T).
 __device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T, float amax) {
-  if (T == 0.f) return 0u;
-  if (!(T >= 0x1p-90f && T <= 0x1p100f && amax <= 8.f * T))
-    return nv_codes8_div(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], T);
-  const float r = __frcp_rn(T);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = div_given_rcp(v[i], T, r);
+  for (int i = 0; i < 8; ++i) y[i] = v[i];
+  nv_quotients(y, T, amax);
   return e2m1x8_rn(y, 1.f);
 }
 

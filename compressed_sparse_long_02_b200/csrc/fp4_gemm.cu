@@ -192,9 +192,7 @@ __device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat,
   uint32_t byte, codes;
   if constexpr (kNv) {
     byte = nv_scale_byte(am, 6.f * g);
-    const float T = e4m3_value(byte) * g;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = T > 0.f ? __fdiv_rn(x[e], T) : 0.f;
+    nv_quotients(x, e4m3_value(byte) * g, am);
     codes = e2m1x2_rn(x[0], x[1]) | e2m1x2_rn(x[2], x[3]) << 8;
   } else {
     const int E = mx_block_exponent(am);
@@ -289,12 +287,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     m0 = mg / p.G * kBN;
   };
 
-  if (threadIdx.x == 0 && first < p.tiles) {
+  if (warp == 2 && first < p.tiles) {  // the hint: a slab per lane
     int n0, g, m0;
     tile(first, n0, g, m0);
-    const int w_row = g * p.N + n0, n = min(slab1 - slab0, 4 * S::kStages);
-    for (int i = 0; i < n; ++i) tma_prefetch_2d(&tm_w, (slab0 + i) * kSlabBytes, w_row);
-    for (int i = 0; i < n; ++i) tma_prefetch_2d(&tm_ws, 0, w_row / 128 * p.w_atoms + (slab0 + i) * S::kAtoms);
+    const int w_row = g * p.N + n0, sl = slab0 + lane;
+    if (sl < slab1) {
+      tma_prefetch_2d(&tm_w, sl * kSlabBytes, w_row);
+      tma_prefetch_2d(&tm_ws, 0, w_row / 128 * p.w_atoms + sl * S::kAtoms);
+    }
   }
   griddep_enter();
 
@@ -412,6 +412,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     int j = 0;
     bool ok = true;
     for (int t = first; ok && t < p.tiles; t += step) {
+      int n0, g, m0;
+      tile(t, n0, g, m0);
       for (int sl = slab0; sl < slab1; ++sl, ++j) {
         const int st = j % S::kStages;
         if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
@@ -419,8 +421,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           break;
         }
         const uint4* src = reinterpret_cast<const uint4*>(sSf + st * S::kBytesSf) + lane;
+        // a tile of 32 or 64 tokens takes its own columns of the row block's four
         constexpr int kUnits = S::kAtoms * (1 + S::kRowBlocks);
         uint32_t r[4 * kUnits];
+        const int sub = kBN < 128 ? m0 % 128 / 32 : 0;
 #pragma unroll
         for (int a = 0; a < S::kAtoms; ++a) {
 #pragma unroll
@@ -428,6 +432,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             const uint4 u = src[32 * (S::kAtoms * b + a)];
             uint32_t* d = r + (b == 0 ? 4 * a : 4 * (S::kAtoms + S::kRowBlocks * a + b - 1));
             d[0] = u.x, d[1] = u.y, d[2] = u.z, d[3] = u.w;
+            if (kBN < 128 && b > 0) {
+              d[0] = sub == 0 ? u.x : (sub == 1 ? u.y : (sub == 2 ? u.z : u.w));
+              if (kBN == 64) d[1] = sub == 0 ? u.y : u.w;
+            }
           }
         }
         const uint32_t dst = dst0 + st * S::kSfCols;
@@ -652,7 +660,7 @@ int resident_pairs(K k, size_t smem, int* cache) {
 }
 
 template <bool kNv, int kBN, int kOut>
-cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
+cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cudaStream_t s) {
   using Sh = Shape<kNv, kBN, kOut>;
   static int smem_set[64], pairs[64];
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
@@ -671,30 +679,60 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s)
   const cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(k), Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const dim3 block(kThreads);
-  p.splits = 1;
   if constexpr (Sh::kPair) {
+    p.splits = 1;
     const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
     return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, p);
   } else {
-    // Split K over 2, 4 or 8 CTAs while the tiles leave SMs (or half SMs) idle and every CTA keeps two slabs or more.
-    const int slabs = (a.K + kSlab - 1) / kSlab, room = num_sms();
-    while (p.splits < 8 && tiles * p.splits * 2 <= room && slabs >= 4 * p.splits) p.splits *= 2;
-    const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, room);
+    p.splits = splits;
+    const int64_t clusters = splits > 1 ? tiles : std::min<int64_t>(tiles, num_sms() * Sh::kMinBlocks);
     const dim3 grid(static_cast<unsigned>(clusters * p.splits));
     if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, p);
     return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, p);
   }
 }
 
+// Tokens per tile and CTAs per tile (a split of K), by the time that each choice would take in
+// nanoseconds beyond what all have in common.  Measured on one B200 (us, 32 / 64 / 128 tokens a
+// tile at their best splits, and pairs): 1 x 4096 x 8192 6.9 / 7.0 / 7.9 / 17; 64 x 4096 x 8192
+// 9.6 / 8.8 / 10.1 / 18; 256 x 4096 x 8192 20 / 14.5 / 14.7 / 18.5; 512 x 4096 x 8192 34 / 21 /
+// 18.7 / 18.7; 600 x 256 x 512, 4 groups, 4.6 / 4.7 / 5.5 / 6.4.  The terms, from the same runs:
+//   a slab of a lone CTA 430 ns, 530 with two on an SM (the latency of its loads, not their
+//   bytes); a slab of a pair 450, and 2000 for its results, which nothing else covers;
+//   a split 400 plus 20 a token (35 at 128 a tile) for the exchanged sums, on a shared SM twice
+//   that and 1500 for a set-up that no longer hides behind the launch before;
+//   unsplit results 10 a token.
+struct Choice {
+  int tokens, splits;
+};
+Choice choose(int M, int N, int K, int G) {
+  const int64_t sms = num_sms(), slabs = (K + kSlab - 1) / kSlab;
+  const int64_t rows = static_cast<int64_t>(G) * ((N + kTileN - 1) / kTileN);
+  const int64_t pairs = static_cast<int64_t>(G) * ((N + 2 * kTileN - 1) / (2 * kTileN)) * ((M + 255) / 256);
+  Choice best{256, 1};
+  int64_t cost = (pairs + sms / 2 - 1) / (sms / 2) * (slabs * 450 + 2000);
+  for (int bn = 32; bn <= 128; bn *= 2) {
+    const int64_t tiles = rows * ((M + bn - 1) / bn), room = bn <= 64 ? 2 * sms : sms, tok = std::min(M, bn);
+    for (int sp = 1; sp <= 8 && sp <= slabs; sp *= 2) {
+      const int64_t ctas = tiles * sp, shared = ctas > sms && bn <= 64 ? 1 : 0;
+      if (sp > 1 && ctas > room) break;
+      const int64_t ends = sp > 1 ? 400 + (bn == 128 ? 35 : 20 * (1 + shared)) * tok + 1500 * shared : 10 * (1 + shared) * tok;
+      const int64_t c = (ctas + room - 1) / room * ((slabs + sp - 1) / sp * (shared ? 530 : 430) + ends);
+      if (c < cost) cost = c, best = Choice{bn, sp};
+    }
+  }
+  return best;
+}
+
 template <bool kNv, int kOut>
 cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  // tokens per tile: the smallest of 32, 64 and 128 that takes them all; beyond 128, pairs of CTAs
-  // once there is a tile for every second pair, else lone 128-token tiles whose K axis can be split
-  const int64_t pairs = (static_cast<int64_t>(a.N) + 255) / 256 * ((a.M + 255) / 256) * a.G;
-  if (a.M > 128 && 4 * pairs >= num_sms()) return launch_tile<kNv, 256, kOut>(a, p, s);
-  if (a.M <= 32) return launch_tile<kNv, 32, kOut>(a, p, s);
-  if (a.M <= 64) return launch_tile<kNv, 64, kOut>(a, p, s);
-  return launch_tile<kNv, 128, kOut>(a, p, s);
+  const Choice c = choose(a.M, a.N, a.K, a.G);
+  switch (c.tokens) {
+    case 32: return launch_tile<kNv, 32, kOut>(a, p, c.splits, s);
+    case 64: return launch_tile<kNv, 64, kOut>(a, p, c.splits, s);
+    case 128: return launch_tile<kNv, 128, kOut>(a, p, c.splits, s);
+    default: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
+  }
 }
 
 }  // namespace

@@ -139,7 +139,9 @@ LINEAR_SHAPES = [  # M, N, K, G: every tile width, ragged rows, features and K, 
     (33, 300, 160, 1), (64, 384, 2080, 1), (65, 129, 4096, 1), (128, 128, 288, 1), (129, 96, 64, 1), (300, 1001, 2080, 1),
     (513, 640, 544, 1), (5, 128, 128, 3), (257, 384, 640, 2), (700, 256, 384, 4), (40, 256, 4096, 8), (2000, 512, 256, 1),
     # pairs of CTAs: ragged features (the second CTA's half empty or cut), tokens and K, groups of an odd half
-    (1700, 1301, 288, 1), (2400, 1153, 96, 1), (1100, 384, 384, 8), (1030, 2560, 2080, 1), (300, 9000, 32, 1)]
+    (1700, 1301, 288, 1), (2400, 1153, 96, 1), (1100, 384, 384, 8), (1030, 2560, 2080, 1), (300, 9000, 32, 1),
+    # many tiles of 64 and of 128 tokens
+    (1000, 1500, 160, 1), (19000, 128, 64, 1), (128, 19100, 64, 1)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
