@@ -8,7 +8,6 @@ Scratch workspaces are torch allocations unless the caller passes one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -145,7 +144,7 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(t: torch.Tensor):
     """The current stream of t's device, without the Stream object (2 us of every call)."""
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(t.get_device()))
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -495,14 +494,11 @@ def _rows_2d(t: torch.Tensor, name: str):
     return rows, cols, ld
 
 
-_here = contextlib.nullcontext()
-
-
-def _on(t: torch.Tensor):
-    """The device guard of a call on t's device (nothing when it is the current one)."""
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether t lives on another CUDA device than the current one (the call then changes over to it)."""
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
-    return _here if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
+    return t.get_device() != torch._C._cuda_getDevice()
 
 
 def csa_fp4_scale_bytes(fmt: str, rows: int, cols: int) -> int:
@@ -533,8 +529,10 @@ def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch
         if out.tensor_scale is not tensor_scale:
             out = out._replace(tensor_scale=tensor_scale)
         m = _fp4_mat(out, "out", dev)
-    with _on(x):
-        st = lib().csa_fp4_quantize(f, x.data_ptr(), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
+    if _elsewhere(x):
+        with torch.cuda.device(dev):
+            return csa_fp4_quantize(x, fmt=fmt, tensor_scale=tensor_scale, out=out)
+    st = lib().csa_fp4_quantize(f, x.data_ptr(), dt, rows, cols, ld, ctypes.byref(m), _stream(x))
     if st:
         _check("csa_fp4_quantize", st)
     return out
@@ -542,16 +540,20 @@ def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch
 
 def csa_fp4_dequantize(m: Fp4Matrix, *, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None):
     """The values of m, [rows, cols] in dtype (float32 or bf16), or into `out` (evenly spaced rows)."""
+    rows, cols, ld = m.rows, m.cols, m.cols
     dev = m.packed.device
     if out is None:
-        out = m.packed.new_empty((m.rows, m.cols), dtype=dtype)
+        out = m.packed.new_empty((rows, cols), dtype=dtype)
+    else:
+        r, c, ld = _rows_2d(out, "out")
+        if r != rows or c != cols or out.device != dev:
+            raise ValueError(f"out must be {rows} x {cols} on {dev}")
     dt = _dt(out)
-    rows, cols, ld = _rows_2d(out, "out")
-    if rows != m.rows or cols != m.cols or out.device != dev:
-        raise ValueError(f"out must be {m.rows} x {m.cols} on {dev}")
-    with _on(out):
-        c = _fp4_mat(m, "m", dev)
-        st = lib().csa_fp4_dequantize(_FP4_FMT[m.fmt], ctypes.byref(c), rows, cols, dt, out.data_ptr(), ld, _stream(out))
+    if _elsewhere(out):
+        with torch.cuda.device(dev):
+            return csa_fp4_dequantize(m, out=out)
+    c = _fp4_mat(m, "m", dev)
+    st = lib().csa_fp4_dequantize(_FP4_FMT[m.fmt], ctypes.byref(c), rows, cols, dt, out.data_ptr(), ld, _stream(out))
     if st:
         _check("csa_fp4_dequantize", st)
     return out
@@ -565,8 +567,10 @@ def csa_fp4_pack_scales(scales: torch.Tensor, cols: int, *, fmt: str = "mxfp4") 
         raise ValueError(f"scales must have {cols} / {_FP4_BLOCK[fmt]} bytes a row, got {tuple(scales.shape)}")
     rows = scales.numel() // scales.shape[-1]
     out = torch.empty(_scale_bytes(fmt, rows, cols), dtype=torch.uint8, device=scales.device)
-    with _on(scales):
-        st = lib().csa_fp4_pack_scales(f, _ptr(scales), rows, cols, _ptr(out), _stream(scales))
+    if _elsewhere(scales):
+        with torch.cuda.device(scales.device):
+            return csa_fp4_pack_scales(scales, cols, fmt=fmt)
+    st = lib().csa_fp4_pack_scales(f, _ptr(scales), rows, cols, _ptr(out), _stream(scales))
     _check("csa_fp4_pack_scales", st)
     return out
 
@@ -574,21 +578,24 @@ def csa_fp4_pack_scales(scales: torch.Tensor, cols: int, *, fmt: str = "mxfp4") 
 def csa_fp4_linear(x: Fp4Matrix, w: Fp4Matrix, *, groups: int = 1, out_dtype: torch.dtype = torch.bfloat16,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """x [M, G K] times w [G N, K] group by group -> y [M, G N] (bf16 or float32)."""
-    dev, fmt, G, M, K = x.packed.device, x.fmt, groups, x.rows, w.cols
+    fmt, M, N, K, dev = x.fmt, x.rows, w.rows, w.cols, x.packed.device
     if fmt != w.fmt:
         raise ValueError(f"x is {fmt} and w is {w.fmt}")
-    if G < 1 or w.rows % G or x.cols != G * K:
-        raise ValueError(f"x {x.rows} x {x.cols} and w {w.rows} x {w.cols} do not fit {G} groups")
+    if groups < 1 or N % groups or x.cols != groups * K:
+        raise ValueError(f"x {M} x {x.cols} and w {N} x {K} do not fit {groups} groups")
     if out is None:
-        out = x.packed.new_empty((M, w.rows), dtype=out_dtype)
+        out, ld = x.packed.new_empty((M, N), dtype=out_dtype), N
+    else:
+        rows, cols, ld = _rows_2d(out, "out")
+        if rows != M or cols != N or out.device != dev:
+            raise ValueError(f"out must be {M} x {N} on {dev}")
     dt = _dt(out)
-    rows, cols, ld = _rows_2d(out, "out")
-    if rows != M or cols != w.rows or out.device != dev:
-        raise ValueError(f"out must be {M} x {w.rows} on {dev}")
-    with _on(out):
-        cx, cw = _fp4_mat(x, "x", dev), _fp4_mat(w, "w", dev)
-        st = lib().csa_fp4_linear(_FP4_FMT[fmt], M, w.rows // G, K, G, ctypes.byref(cx), ctypes.byref(cw), dt,
-                                  out.data_ptr(), ld, _stream(out))
+    if _elsewhere(out):
+        with torch.cuda.device(dev):
+            return csa_fp4_linear(x, w, groups=groups, out=out)
+    cx, cw = _fp4_mat(x, "x", dev), _fp4_mat(w, "w", dev)
+    st = lib().csa_fp4_linear(_FP4_FMT[fmt], M, N // groups, K, groups, ctypes.byref(cx), ctypes.byref(cw), dt,
+                              out.data_ptr(), ld, _stream(out))
     if st:
         _check("csa_fp4_linear", st)
     return out
@@ -619,12 +626,15 @@ def csa_grouped_out_proj_fp4(o: torch.Tensor, A: Fp4Matrix, Bm: Fp4Matrix, *, gr
         workspace = o.new_empty(csa_grouped_out_proj_fp4_workspace(fmt, T, H, D, G, R), dtype=torch.uint8)
     if out.device != dev or workspace.device != dev:
         raise ValueError(f"out and workspace must be on {dev}")
-    with _on(o):
-        ca, cb = _fp4_mat(A, "A", dev), _fp4_mat(Bm, "Bm", dev)
-        st = lib().csa_grouped_out_proj_fp4(_FP4_FMT[fmt], T, H, D, G, R, d_model, _ptr(o),
-                                            _tensor_scale(fmt, o_scale, dev, "o_scale"), ctypes.byref(ca),
-                                            _tensor_scale(fmt, z_scale, dev, "z_scale"), ctypes.byref(cb), _ptr(out),
-                                            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(o))
+    if _elsewhere(o):
+        with torch.cuda.device(dev):
+            return csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=o_scale, z_scale=z_scale, out=out,
+                                            workspace=workspace)
+    ca, cb = _fp4_mat(A, "A", dev), _fp4_mat(Bm, "Bm", dev)
+    st = lib().csa_grouped_out_proj_fp4(_FP4_FMT[fmt], T, H, D, G, R, d_model, _ptr(o),
+                                        _tensor_scale(fmt, o_scale, dev, "o_scale"), ctypes.byref(ca),
+                                        _tensor_scale(fmt, z_scale, dev, "z_scale"), ctypes.byref(cb), _ptr(out),
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(o))
     if st:
         _check("csa_grouped_out_proj_fp4", st)
     return out
