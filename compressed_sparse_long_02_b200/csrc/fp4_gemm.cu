@@ -11,10 +11,10 @@
 // axis (kBN a tile), so a single decode token (kBN = 32) streams the weights once and pads
 // nothing to 128 rows.  A K slab is 256 elements = 128 bytes a row, one swizzle row.
 //
-// Roles (448 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks);
-// warp 1 owns TMEM and one thread of it issues the MMAs; warps 2-9 write the results (two warps
+// Roles (512 threads): warp 0 issues the TMA loads (codes, and scale atoms as 512-byte blocks);
+// warp 1 owns TMEM and one thread of it issues the MMAs; warps 8-15 write the results (two warps
 // per TMEM lane quarter, half of the tile's tokens each; a lane holds one output feature);
-// warps 10-13 bring each slab's scales from shared memory to TMEM.  The scales go by
+// warps 4-7 bring each slab's scales from shared memory to TMEM.  The scales go by
 // tcgen05.st: a lane's 16 bytes of an atom are its four columns.  tcgen05.cp from the MMA thread
 // runs in order with the MMAs and cost 50-60 cycles per 512-byte atom, 370 (MXFP4) or 650
 // (NVFP4) cycles next to a 256 x 256 slab's 512 cycles of MMAs; the stores run beside them.
@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -51,17 +52,22 @@ namespace {
 constexpr int kTileN = 128;          // output features of a tile (MMA M)
 constexpr int kSlabBytes = 128;      // bytes of a row in a K slab: 256 elements
 constexpr int kSlab = 2 * kSlabBytes;
-constexpr int kThreads = 448;
-constexpr int kSfWarp = 10;          // first of the four scale warps
+constexpr int kThreads = 512;
+constexpr int kHintWarp = 2;         // asks for the first tile's weights in L2
+constexpr int kSfWarp = 4;           // first of the four scale warps
+constexpr int kOutWarp = 8;          // first of the eight result warps
 
 enum Out { kOutF32, kOutBf16, kOutFp4 };
 
 template <bool kNv, int kBN, int kOut>
 struct Shape {
-  static constexpr bool kPair = kBN == 256;
+  static constexpr bool kPair = kBN >= 256;
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kAtoms = kNv ? 4 : 2;                   // scale atoms of a slab per 128 rows
-  static constexpr int kRowBlocks = kBN > 128 ? 2 : 1;         // 128-row scale blocks of the tokens
+  static constexpr int kRowBlocks = (kBN + 127) / 128;         // 128-row scale blocks of the tokens
+  static constexpr int kN0 = kBN < 256 ? kBN : 256;            // tokens of the first MMA of a K step,
+  static constexpr int kN1 = kBN - kN0;                        // and of the second (384: 256 + 128)
+  static constexpr int kBoxX = kBN == 384 ? 64 : kBN / kCtas;  // tokens of one load
   static constexpr int kRowsX = kBN / kCtas;                   // tokens that a CTA loads
   static constexpr uint32_t kBytesW = kTileN * kSlabBytes;     // 16 KB
   static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
@@ -78,10 +84,19 @@ struct Shape {
   static constexpr int kAcc = kPair ? 1 : 2;                   // accumulators of kBN columns
   static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);  // TMEM columns of a slab's scales
   static constexpr uint32_t kColSf = kAcc * kBN;
-  static constexpr uint32_t kCols = kColSf + kStages * kSfCols;  // a slot of scales per stage
+  // a slot of scales per stage, or as many as fit
+  static constexpr int kRoom = static_cast<int>((512 / kMinBlocks - kColSf) / kSfCols);
+  static constexpr int kSlots = kRoom < kStages ? kRoom : kStages;
+  static constexpr uint32_t kCols = kColSf + kSlots * kSfCols;
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= kTmem && kTmem * kMinBlocks <= 512, "TMEM budget");
   static_assert((kSmem + 1024) * kMinBlocks <= 228 * 1024, "shared memory budget");
+  static_assert(kSlots >= 2, "scales double-buffered");
+  // Registers of a thread after the split, by warpgroup (launched with 65536 / 512 / kMinBlocks each):
+  // loads and MMAs, scales, results (two).
+  static constexpr int kRegsIssue = kMinBlocks == 1 ? 56 : 40, kRegsSf = kMinBlocks == 1 ? 96 : 56;
+  static constexpr int kRegsOut = kMinBlocks == 1 ? 176 : 80;
+  static_assert(kRegsIssue + kRegsSf + 2 * kRegsOut <= 4 * (128 / kMinBlocks), "register budget");
 };
 
 struct LinearParams {
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     m0 = mg / p.G * kBN;
   };
 
-  if (warp == 2 && first < p.tiles) {  // the hint: a slab per lane
+  if (warp == kHintWarp && first < p.tiles) {  // the hint: a slab per lane
     int n0, g, m0;
     tile(first, n0, g, m0);
     const int w_row = g * p.N + n0, sl = slab0 + lane;
@@ -298,7 +313,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   }
   griddep_enter();
 
-  if (warp == 0) {
+  if (warp < kSfWarp) {
+   regs_dec<S::kRegsIssue>();
+   if (warp == 0) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       int j = 0;
@@ -307,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         int n0, g, m0;
         tile(t, n0, g, m0);
         const int w_row = g * p.N + n0;
-        const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);
+        // a pair's MMA takes half of its tokens from each CTA
+        const int x_row0 = m0 + (kPair ? rank * S::kN0 / 2 : 0), x_row1 = m0 + S::kN0 + rank * S::kN1 / 2;
         const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
@@ -328,10 +346,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           if constexpr (kPair) {
             const uint32_t bar = dsmem_map(&full[st], 0);
             tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
-            tma_load_2d_pair(dx, &tm_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
+            const int x_col = g * (p.K / 2) + sl * kSlabBytes;
+#pragma unroll
+            for (int r = 0; r < S::kRowsX; r += S::kBoxX)
+              tma_load_2d_pair(dx + r * kSlabBytes, &tm_x, bar, x_col, r < S::kN0 / 2 ? x_row0 + r : x_row1 + r - S::kN0 / 2);
           } else {
             tma_load_2d(dw, &tm_w, &full[st], sl * kSlabBytes, w_row);
-            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
+            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row0);
           }
         }
       }
@@ -344,69 +365,86 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0 && leader) {
+    // The whole warp runs the loop and one lane is elected per slab: with a loop inside `lane == 0`
+    // the MMAs of a slab left the tensor pipe idle between them (698 against 512 cycles for a
+    // pair's slab, measured without loads).
+    if (leader) {
       int j = 0, it = 0;
       bool ok = true;
       for (int t = first; ok && t < p.tiles; t += step, ++it) {
         const int buf = it % S::kAcc;
-        if (!mbar_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag)) break;
+        if (!warp_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag)) break;
         tc_fence_after();
         const uint32_t acc = tmem + kBN * buf;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
           const uint32_t ph = (j / S::kStages) & 1;
-          if (!mbar_wait(&sf_ready[st], ph, p.err, abort_flag) || !mbar_wait(&full[st], ph, p.err, abort_flag)) {
+          if (!warp_wait(&sf_ready[st], ph, p.err, abort_flag) || !warp_wait(&full[st], ph, p.err, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
-          const uint32_t sfw = tmem + S::kColSf + st * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
+          const uint32_t sfw = tmem + S::kColSf + j % S::kSlots * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
           const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
-          auto mma = [&](int kk) {
+          auto mma_n = [&](int kk, auto n_tag, uint32_t d, uint32_t b1, uint32_t sfb) {
+            constexpr int kN = decltype(n_tag)::value, kRows = kTileN * S::kCtas;
             const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
-            const uint64_t db = smem_desc(b0 + 32 * kk, 16, 1024, kSwizzle128B);
+            const uint64_t db = smem_desc(b1 + 32 * kk, 16, 1024, kSwizzle128B);
             const uint32_t accumulate = (sl > slab0 || kk > 0) ? 1u : 0u;
-            constexpr int kRows = kTileN * S::kCtas;
             if constexpr (kNv) {
-              const uint32_t a = sfw + 4 * kk, b = sfx + 4 * S::kRowBlocks * kk;
+              const uint32_t a = sfw + 4 * kk, b = sfb + 4 * S::kRowBlocks * kk;
               if constexpr (kPair)
-                mma_nvf4_pair(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
+                mma_nvf4_pair(d, da, db, idesc_nvf4(kRows, kN), accumulate, a, b);
               else
-                mma_nvf4(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
+                mma_nvf4(d, da, db, idesc_nvf4(kRows, kN), accumulate, a, b);
             } else {
               const uint32_t id = 2 * (kk & 1);  // the byte of the scale column of this K = 64 step
-              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
+              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfb + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
               if constexpr (kPair)
-                mma_mxf4_pair(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
+                mma_mxf4_pair(d, da, db, idesc_mxf4(kRows, kN, id, id), accumulate, a, b);
               else
-                mma_mxf4(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
+                mma_mxf4(d, da, db, idesc_mxf4(kRows, kN, id, id), accumulate, a, b);
             }
           };
-          if (n_mma == 4) {
+          auto mma = [&](int kk) {
+            mma_n(kk, std::integral_constant<int, S::kN0>{}, acc, b0, sfx);
+            if constexpr (S::kN1 > 0)
+              mma_n(kk, std::integral_constant<int, S::kN1>{}, acc + S::kN0, b0 + S::kN0 / 2 * kSlabBytes, sfx + S::kN0 / 32);
+          };
+          if (elect_one()) {
+            if (n_mma == 4) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma(kk);
-          } else {
-            for (int kk = 0; kk < n_mma; ++kk) mma(kk);
+              for (int kk = 0; kk < 4; ++kk) mma(kk);
+            } else {
+              for (int kk = 0; kk < n_mma; ++kk) mma(kk);
+            }
+            commit(&empty[st]);
+            if (sl == slab1 - 1) commit(&acc_full[buf]);
           }
-          commit(&empty[st]);
+          __syncwarp();
         }
-        if (ok) commit(&acc_full[buf]);
       }
-      if constexpr (kPair)
-        tc_commit_pair_local(fin);
-      else
-        tc_commit(fin);
+      if (elect_one()) {
+        if constexpr (kPair)
+          tc_commit_pair_local(fin);
+        else
+          tc_commit(fin);
+      }
+      __syncwarp();
       volatile int never = 0;
       mbar_wait(fin, 0, p.err, &never);
     }
     __syncwarp();
-  } else if (warp >= kSfWarp) {
-    // ---------------------------------------------------------------- scales to TMEM (warps 10-13)
+   }
+  } else if (warp < kOutWarp) {
+    regs_dec<S::kRegsSf>();
+    // ---------------------------------------------------------------- scales to TMEM (warps 4-7)
     // slot of a stage: W in columns [0, 4 kAtoms) (4 per atom), then X (per atom 4 per row block).
-    // The stage is loaded again only after the MMAs that read the slot, so the slot is free too.
+    // With a slot per stage, the stage is loaded again only after the MMAs that read the slot, so the
+    // slot is free too; with fewer, the MMAs that read it are waited for.
     const uint32_t dst0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + S::kColSf;
     const uint32_t ready0 = kPair ? dsmem_map(sf_ready, 0) : 0u;
     int j = 0;
@@ -419,6 +457,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
           ok = false;
           break;
+        }
+        if constexpr (S::kSlots < S::kStages) {
+          const int i = j - S::kSlots;
+          if (i >= 0 && !warp_wait(&empty[i % S::kStages], (i / S::kStages) & 1, p.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
         }
         const uint4* src = reinterpret_cast<const uint4*>(sSf + st * S::kBytesSf) + lane;
         // a tile of 32 or 64 tokens takes its own columns of the row block's four
@@ -438,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             }
           }
         }
-        const uint32_t dst = dst0 + st * S::kSfCols;
-        static_assert(4 * kUnits == 16 || 4 * kUnits == 24 || 4 * kUnits == 32 || 4 * kUnits == 48, "store widths");
+        const uint32_t dst = dst0 + j % S::kSlots * S::kSfCols;
+        static_assert(4 * kUnits <= 64 && 4 * kUnits % 8 == 0 && 4 * kUnits % 32 != 8, "store widths");
         if constexpr (4 * kUnits >= 32) tmem_st32(dst, r);
+        if constexpr (4 * kUnits == 64) tmem_st32(dst + 32, r + 32);
         if constexpr (4 * kUnits % 32 >= 16) tmem_st16(dst + 4 * kUnits / 32 * 32, r + 4 * kUnits / 32 * 32);
         if constexpr (4 * kUnits % 16 == 8) tmem_st8(dst + 16, r + 16);
         tmem_wait_st();
@@ -455,14 +502,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
       }
     }
   } else {
-    // ---------------------------------------------------------------- results (warps 2-9)
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    regs_inc<S::kRegsOut>();
+    // ---------------------------------------------------------------- results (warps 8-15)
+    const int quarter = warp & 3, half = (warp - kOutWarp) >> 2;
     constexpr int kHalf = kBN / 2;
     const int f = 32 * quarter + lane, c0 = half * kHalf;  // this lane's feature, this warp's first token of a tile
     const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
     const float gz = kOut == kOutFp4 && kNv ? __ldg(p.gz) : 1.f;
     const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
-    if (!kPair && p.splits > 1 && warp == 2 && lane == 0) {  // the bytes this CTA will receive
+    if (!kPair && p.splits > 1 && warp == kOutWarp && lane == 0) {  // the bytes this CTA will receive
       int n0, g, m0;
       tile(first, n0, g, m0);
       const int m_valid = min(kBN, p.M - m0), cap = (m_valid + p.splits - 1) / p.splits;
@@ -513,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         if (p.splits == 1 ? named_bar_or(1, 256, !got) : !warp_wait(recv_full, 0, p.err, abort_flag)) break;
         // a warp takes a token at a time: four features per lane, the partials added in rank order
         const int tok0 = p.splits > 1 ? rank * cap : 0, n_tok = p.splits > 1 ? min(cap, m_valid - rank * cap) : m_valid;
-        for (int i = warp - 2; i < n_tok; i += 8) {
+        for (int i = warp - kOutWarp; i < n_tok; i += 8) {
           const float* part = recv + i * kTileN + 4 * lane;
           float4 sum = *reinterpret_cast<const float4*>(part);
           for (int r = 1; r < p.splits; ++r) {
@@ -540,28 +588,29 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
       } else if constexpr (kOut == kOutF32) {
         const int n = n0 + f;
         float* y = static_cast<float*>(p.y) + static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
-#pragma unroll 1
-        for (int c = 0; c < kHalf; c += 16) {
-          uint32_t u[16];
-          tmem_ld16(src + c, u);
-          tmem_wait_ld();
-          if (c + 16 == kHalf) release();
-          if (n < p.N) {
+        uint32_t v[kHalf];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < m_left) y[(c + i) * p.ldy] = __uint_as_float(u[i]) * alpha;
+        for (int c = 0; c < kHalf; c += 16) tmem_ld16(src + c, v + c);
+        tmem_wait_ld();
+        release();
+        if (n < p.N) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            if (i < m_left) *y = __uint_as_float(v[i]) * alpha;
+            y += p.ldy;
           }
         }
       } else {
         // the warp's whole share rounded to bf16 in registers, then stored while the next tile runs
         uint32_t v[kHalf / 2];
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 16) {
-          uint32_t u[16];
+        for (int c = 0; c < kHalf; c += 32) {
+          uint32_t u[32];
           tmem_ld16(src + c, u);
+          tmem_ld16(src + c + 16, u + 16);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 16; ++i)
             v[c / 2 + i] = fp4_bf16x2(__uint_as_float(u[2 * i]) * alpha, __uint_as_float(u[2 * i + 1]) * alpha);
         }
         release();
@@ -571,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           // 64 tokens at a time among the four warps of this half, whose lanes hold all 128 features
           uint4* buf_z = reinterpret_cast<uint4*>(recv) + half * 64 * 16;
           uint32_t* buf_w = reinterpret_cast<uint32_t*>(buf_z);
-          const int odd = lane & 1, id = (warp - 2) % 4 * 32 + lane;
+          const int odd = lane & 1, id = quarter * 32 + lane;
 #pragma unroll
           for (int part = 0; part < kHalf / 64; ++part) {
             named_bar_sync(1 + half, 128);  // the last readers are done
@@ -665,7 +714,7 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
   static int smem_set[64], pairs[64];
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
-  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kBoxX, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
       !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
@@ -731,7 +780,12 @@ cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s
     case 32: return launch_tile<kNv, 32, kOut>(a, p, c.splits, s);
     case 64: return launch_tile<kNv, 64, kOut>(a, p, c.splits, s);
     case 128: return launch_tile<kNv, 128, kOut>(a, p, c.splits, s);
-    default: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
+    case 256: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
+  }
+  if constexpr (kOut != kOutF32) {
+    return launch_tile<kNv, 384, kOut>(a, p, 1, s);
+  } else {
+    return launch_tile<kNv, 256, kOut>(a, p, 1, s);
   }
 }
 

@@ -168,6 +168,18 @@ __device__ __forceinline__ bool named_bar_or(int id, int n, bool pred) {
   return r != 0;
 }
 
+// ------------------------------------------------------------------ register split
+// Every warp of a warpgroup (four warps, the first a multiple of four) gives up or takes registers;
+// what the warpgroups end with must not exceed what the block was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ------------------------------------------------------------------ cp.async (LSU path)
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
   // src-size 0 fills the 16 destination bytes with zeros
@@ -485,6 +497,17 @@ __device__ __forceinline__ void st_async_u32(uint32_t addr, uint32_t v, uint32_t
 }
 
 // ------------------------------------------------------------------ misc
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
 
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
