@@ -38,7 +38,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -61,13 +60,10 @@ enum Out { kOutF32, kOutBf16, kOutFp4 };
 
 template <bool kNv, int kBN, int kOut>
 struct Shape {
-  static constexpr bool kPair = kBN >= 256;
+  static constexpr bool kPair = kBN == 256;
   static constexpr int kCtas = kPair ? 2 : 1;
   static constexpr int kAtoms = kNv ? 4 : 2;                   // scale atoms of a slab per 128 rows
   static constexpr int kRowBlocks = (kBN + 127) / 128;         // 128-row scale blocks of the tokens
-  static constexpr int kN0 = kBN < 256 ? kBN : 256;            // tokens of the first MMA of a K step,
-  static constexpr int kN1 = kBN - kN0;                        // and of the second (384: 256 + 128)
-  static constexpr int kBoxX = kBN == 384 ? 64 : kBN / kCtas;  // tokens of one load
   static constexpr int kRowsX = kBN / kCtas;                   // tokens that a CTA loads
   static constexpr uint32_t kBytesW = kTileN * kSlabBytes;     // 16 KB
   static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
@@ -84,14 +80,10 @@ struct Shape {
   static constexpr int kAcc = kPair ? 1 : 2;                   // accumulators of kBN columns
   static constexpr uint32_t kSfCols = 4 * kAtoms * (1 + kRowBlocks);  // TMEM columns of a slab's scales
   static constexpr uint32_t kColSf = kAcc * kBN;
-  // a slot of scales per stage, or as many as fit
-  static constexpr int kRoom = static_cast<int>((512 / kMinBlocks - kColSf) / kSfCols);
-  static constexpr int kSlots = kRoom < kStages ? kRoom : kStages;
-  static constexpr uint32_t kCols = kColSf + kSlots * kSfCols;
+  static constexpr uint32_t kCols = kColSf + kStages * kSfCols;  // a slot of scales per stage
   static constexpr uint32_t kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= kTmem && kTmem * kMinBlocks <= 512, "TMEM budget");
   static_assert((kSmem + 1024) * kMinBlocks <= 228 * 1024, "shared memory budget");
-  static_assert(kSlots >= 2, "scales double-buffered");
   // Registers of a thread after the split, by warpgroup (launched with 65536 / 512 / kMinBlocks each):
   // loads and MMAs, scales, results (two).
   static constexpr int kRegsIssue = kMinBlocks == 1 ? 56 : 40, kRegsSf = kMinBlocks == 1 ? 96 : 56;
@@ -324,8 +316,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         int n0, g, m0;
         tile(t, n0, g, m0);
         const int w_row = g * p.N + n0;
-        // a pair's MMA takes half of its tokens from each CTA
-        const int x_row0 = m0 + (kPair ? rank * S::kN0 / 2 : 0), x_row1 = m0 + S::kN0 + rank * S::kN1 / 2;
+        const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);  // a pair's MMA takes half of its tokens from each CTA
         const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
@@ -346,13 +337,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           if constexpr (kPair) {
             const uint32_t bar = dsmem_map(&full[st], 0);
             tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
-            const int x_col = g * (p.K / 2) + sl * kSlabBytes;
-#pragma unroll
-            for (int r = 0; r < S::kRowsX; r += S::kBoxX)
-              tma_load_2d_pair(dx + r * kSlabBytes, &tm_x, bar, x_col, r < S::kN0 / 2 ? x_row0 + r : x_row1 + r - S::kN0 / 2);
+            tma_load_2d_pair(dx, &tm_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
           } else {
             tma_load_2d(dw, &tm_w, &full[st], sl * kSlabBytes, w_row);
-            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row0);
+            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
           }
         }
       }
@@ -387,32 +375,27 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           }
           tc_fence_after();
           const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
-          const uint32_t sfw = tmem + S::kColSf + j % S::kSlots * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
+          const uint32_t sfw = tmem + S::kColSf + st * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
           const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
-          auto mma_n = [&](int kk, auto n_tag, uint32_t d, uint32_t b1, uint32_t sfb) {
-            constexpr int kN = decltype(n_tag)::value, kRows = kTileN * S::kCtas;
+          auto mma = [&](int kk) {
             const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
-            const uint64_t db = smem_desc(b1 + 32 * kk, 16, 1024, kSwizzle128B);
+            const uint64_t db = smem_desc(b0 + 32 * kk, 16, 1024, kSwizzle128B);
             const uint32_t accumulate = (sl > slab0 || kk > 0) ? 1u : 0u;
+            constexpr int kRows = kTileN * S::kCtas;
             if constexpr (kNv) {
-              const uint32_t a = sfw + 4 * kk, b = sfb + 4 * S::kRowBlocks * kk;
+              const uint32_t a = sfw + 4 * kk, b = sfx + 4 * S::kRowBlocks * kk;
               if constexpr (kPair)
-                mma_nvf4_pair(d, da, db, idesc_nvf4(kRows, kN), accumulate, a, b);
+                mma_nvf4_pair(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
               else
-                mma_nvf4(d, da, db, idesc_nvf4(kRows, kN), accumulate, a, b);
+                mma_nvf4(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
             } else {
               const uint32_t id = 2 * (kk & 1);  // the byte of the scale column of this K = 64 step
-              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfb + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
+              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
               if constexpr (kPair)
-                mma_mxf4_pair(d, da, db, idesc_mxf4(kRows, kN, id, id), accumulate, a, b);
+                mma_mxf4_pair(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
               else
-                mma_mxf4(d, da, db, idesc_mxf4(kRows, kN, id, id), accumulate, a, b);
+                mma_mxf4(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
             }
-          };
-          auto mma = [&](int kk) {
-            mma_n(kk, std::integral_constant<int, S::kN0>{}, acc, b0, sfx);
-            if constexpr (S::kN1 > 0)
-              mma_n(kk, std::integral_constant<int, S::kN1>{}, acc + S::kN0, b0 + S::kN0 / 2 * kSlabBytes, sfx + S::kN0 / 32);
           };
           if (elect_one()) {
             if (n_mma == 4) {
@@ -443,8 +426,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     regs_dec<S::kRegsSf>();
     // ---------------------------------------------------------------- scales to TMEM (warps 4-7)
     // slot of a stage: W in columns [0, 4 kAtoms) (4 per atom), then X (per atom 4 per row block).
-    // With a slot per stage, the stage is loaded again only after the MMAs that read the slot, so the
-    // slot is free too; with fewer, the MMAs that read it are waited for.
+    // The stage is loaded again only after the MMAs that read the slot, so the slot is free too.
     const uint32_t dst0 = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + S::kColSf;
     const uint32_t ready0 = kPair ? dsmem_map(sf_ready, 0) : 0u;
     int j = 0;
@@ -457,14 +439,6 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
           ok = false;
           break;
-        }
-        if constexpr (S::kSlots < S::kStages) {
-          const int i = j - S::kSlots;
-          if (i >= 0 && !warp_wait(&empty[i % S::kStages], (i / S::kStages) & 1, p.err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
         }
         const uint4* src = reinterpret_cast<const uint4*>(sSf + st * S::kBytesSf) + lane;
         // a tile of 32 or 64 tokens takes its own columns of the row block's four
@@ -484,10 +458,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             }
           }
         }
-        const uint32_t dst = dst0 + j % S::kSlots * S::kSfCols;
-        static_assert(4 * kUnits <= 64 && 4 * kUnits % 8 == 0 && 4 * kUnits % 32 != 8, "store widths");
+        const uint32_t dst = dst0 + st * S::kSfCols;
+        static_assert(4 * kUnits <= 48 && 4 * kUnits % 8 == 0, "store widths");
         if constexpr (4 * kUnits >= 32) tmem_st32(dst, r);
-        if constexpr (4 * kUnits == 64) tmem_st32(dst + 32, r + 32);
         if constexpr (4 * kUnits % 32 >= 16) tmem_st16(dst + 4 * kUnits / 32 * 32, r + 4 * kUnits / 32 * 32);
         if constexpr (4 * kUnits % 16 == 8) tmem_st8(dst + 16, r + 16);
         tmem_wait_st();
@@ -714,7 +687,7 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
   static int smem_set[64], pairs[64];
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
-  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kBoxX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
       !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
@@ -751,6 +724,8 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
 //   a split 400 plus 20 a token (35 at 128 a tile) for the exchanged sums, on a shared SM twice
 //   that and 1500 for a set-up that no longer hides behind the launch before;
 //   unsplit results 10 a token.
+// In batch-invariant mode K is never split, so a row's sums run over K in one order whatever the
+// number of rows.
 struct Choice {
   int tokens, splits;
 };
@@ -762,7 +737,7 @@ Choice choose(int M, int N, int K, int G) {
   int64_t cost = (pairs + sms / 2 - 1) / (sms / 2) * (slabs * 450 + 2000);
   for (int bn = 32; bn <= 128; bn *= 2) {
     const int64_t tiles = rows * ((M + bn - 1) / bn), room = bn <= 64 ? 2 * sms : sms, tok = std::min(M, bn);
-    for (int sp = 1; sp <= 8 && sp <= slabs; sp *= 2) {
+    for (int sp = 1; sp <= (batch_invariant() ? 1 : 8) && sp <= slabs; sp *= 2) {
       const int64_t ctas = tiles * sp, shared = ctas > sms && bn <= 64 ? 1 : 0;
       if (sp > 1 && ctas > room) break;
       const int64_t ends = sp > 1 ? 400 + (bn == 128 ? 35 : 20 * (1 + shared)) * tok + 1500 * shared : 10 * (1 + shared) * tok;
@@ -780,12 +755,7 @@ cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s
     case 32: return launch_tile<kNv, 32, kOut>(a, p, c.splits, s);
     case 64: return launch_tile<kNv, 64, kOut>(a, p, c.splits, s);
     case 128: return launch_tile<kNv, 128, kOut>(a, p, c.splits, s);
-    case 256: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
-  }
-  if constexpr (kOut != kOutF32) {
-    return launch_tile<kNv, 384, kOut>(a, p, 1, s);
-  } else {
-    return launch_tile<kNv, 256, kOut>(a, p, 1, s);
+    default: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
   }
 }
 

@@ -423,8 +423,9 @@ CSA_API csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales
  *   y[m, g N + n] = gx gw sum_k X[m, g K + k] W[g N + n, k],   g < G, n < N, k < K
  * x: [M, G K]; w: [G N, K]; y: [M, ldy] in y_dtype, ldy >= G N (columns past G N are left as they
  * are).  One call for every M, from a decode token to a prefill.  float32 accumulation, one
- * rounding to y_dtype; the result does not depend on timing, but it may differ between values of
- * M (the K axis is split over CTAs when there are few tiles).
+ * rounding to y_dtype.  The result never depends on timing; it may differ with M in the last
+ * bits, since K is split over CTAs when there are few tiles (never with csa_set_batch_invariant
+ * on: a row's result is then the same whatever the other rows).
  * Supported: K a multiple of 32; with G > 1, K and N multiples of 128.  No workspace.
  */
 CSA_API csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x,
@@ -454,7 +455,8 @@ CSA_API csa_status csa_get_device_error(int32_t* code_out, cudaStream_t stream);
  * the fewest power-of-two parts of at most 512 rows (at most 8 parts), a rule that
  * depends on k + W (or E_max + W) only.  A query's output is then bitwise the same
  * whatever batch it is computed in, and the decode calls reproduce the prefill's
- * outputs bit for bit.  Every other call is batch-invariant already: indexer scores
+ * outputs bit for bit.  csa_fp4_linear and csa_grouped_out_proj_fp4 then never split K.
+ * Every other call is batch-invariant already: indexer scores
  * are a fixed per-pair chain, top-k is exact, and csa_compress_step writes
  * csa_compress's entries.  The workspace sizes follow the setting: query them after
  * setting it.

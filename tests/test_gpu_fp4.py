@@ -7,6 +7,10 @@ addition of a K = 64 step's sum per step, each within 2^-23 of the running sums,
 sum |x w| -- plus the rounding of the result (half a step: 2^-8 relative in bf16, 2^-24 in
 float32) and three float32 products with the tensor scales.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -302,3 +306,54 @@ def test_nan_and_infinite_scales_reach_only_their_rows(B, cuda):
     y = B.csa_fp4_linear(m, B.Fp4Matrix("mxfp4", 150, 160, w.packed, sc))
     keep = torch.arange(150, device=cuda) != 3
     assert y[:, 3].isnan().all() and torch.equal(y[:, keep], ref[:, keep])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_batch_invariant_rows(B, cuda, fmt):
+    """With the switch on, a row's result is the same bits whatever the number of rows (every tile
+    width, lone CTAs and pairs), in the product and in the projection."""
+    rng = np.random.default_rng(8)
+    M, N, K = 3000, 1536, 4128
+    mx, _ = make(B, cuda, rng, M, K, fmt)
+    mw, _ = make(B, cuda, rng, N, K, fmt, K ** -0.5)
+    o = torch.randn((M, 8, 64), device=cuda).to(torch.bfloat16)
+    A, _ = make(B, cuda, rng, 2 * 128, 256, fmt, 0.06)
+    Bm, _ = make(B, cuda, rng, 300, 256, fmt, 0.06)
+    g = torch.tensor([6.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    first = lambda m: B.csa_fp4_quantize(B.csa_fp4_dequantize(mx, dtype=torch.float32)[:m], fmt=fmt, tensor_scale=mx.tensor_scale)  # noqa: E731
+    try:
+        B.csa_set_batch_invariant(True)
+        whole = B.csa_fp4_linear(first(M), mw, out_dtype=torch.float32)
+        proj = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=2, o_scale=g, z_scale=g)
+        for m in (1, 33, 100, 130, 700):
+            assert torch.equal(B.csa_fp4_linear(first(m), mw, out_dtype=torch.float32), whole[:m]), m
+            assert torch.equal(B.csa_grouped_out_proj_fp4(o[:m], A, Bm, groups=2, o_scale=g, z_scale=g), proj[:m]), m
+    finally:
+        B.csa_set_batch_invariant(False)
+    assert B.csa_get_device_error() == 0
+
+
+def test_first_call_inside_a_capture(cuda):
+    """A process whose first call of the products is captured: the replay gives what an eager call does."""
+    code = """
+import torch
+from compressed_sparse_long_02_b200 import binding as B
+dev = torch.device("cuda:0")
+x, o = torch.randn((40, 512), device=dev), torch.randn((700, 8, 64), device=dev).to(torch.bfloat16)
+w = B.csa_fp4_quantize(torch.randn((1024, 512), device=dev))
+A, Bm = B.csa_fp4_quantize(torch.randn((512, 256), device=dev)), B.csa_fp4_quantize(torch.randn((1000, 512), device=dev))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = B.csa_fp4_linear(B.csa_fp4_quantize(x), w)
+    z = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=2)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, B.csa_fp4_linear(B.csa_fp4_quantize(x), w))
+assert torch.equal(z, B.csa_grouped_out_proj_fp4(o, A, Bm, groups=2))
+assert B.csa_get_device_error() == 0
+print("captured ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
