@@ -77,7 +77,7 @@ struct RowTask {
     }
   }
   // stores the codes (where `in`) and returns the atom's four scale bytes, in each of its lanes
-  __device__ __forceinline__ uint32_t encode(float g, float six_g, uint8_t* packed, int64_t at, bool in) const {
+  __device__ __forceinline__ uint32_t encode(const NvScale& nv, uint8_t* packed, int64_t at, bool in) const {
     const int lane = threadIdx.x & 31;
     float am = raw[0].amax();
 #pragma unroll
@@ -87,8 +87,8 @@ struct RowTask {
     uint32_t byte, word[kUnits];
     float T = 0.f;
     if constexpr (kNv) {
-      byte = nv_scale_byte(am, six_g);
-      T = e4m3_value(byte) * g;
+      byte = nv.byte(am);
+      T = e4m3_value(byte) * nv.g;
     } else {
       const int E = mx_block_exponent(am);
       T = mx_pow2_neg(E);
@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * kFp4Threads + threadIdx.x) >> 5;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * (kFp4Threads / 32);
-  const float g = kNv ? __ldg(tensor_scale) : 1.f;
-  const float six_g = 6.f * g;
+  const NvScale nv(kNv ? __ldg(tensor_scale) : 1.f);
   for (Task t(warp0, n_warps, p.n_chunks); t.row < p.n_rows32; t.next(p.n_chunks)) {
     const int r32 = t.row & 31;
     const int64_t row0 = (t.row >> 5) * 128 + r32;
@@ -136,13 +135,13 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
 #pragma unroll
       for (int i = 0; i < 4; ++i) rt[i].load(x, (row0 + 32 * i) * p.ld + col, in);  // every load first
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(g, six_g, packed, (row0 + 32 * i) * p.cols + col, in);
+      for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(nv, packed, (row0 + 32 * i) * p.cols + col, in);
     } else {  // the last row block: one row at a time, so that rows that only pad it cost nothing
 #pragma unroll 1
       for (int64_t row = row0; row < p.rows; row += 32) {
         RT rt;
         rt.load(x, row * p.ld + col, in);
-        const uint32_t v = rt.encode(g, six_g, packed, row * p.cols + col, in);
+        const uint32_t v = rt.encode(nv, packed, row * p.cols + col, in);
         const int i = static_cast<int>((row - row0) / 32);
         w[0] = i == 0 ? v : w[0];
         w[1] = i == 1 ? v : w[1];

@@ -27,11 +27,6 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {  // exact; 0x7F / 0
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
-// NVFP4 scale byte of a block: e4m3(amax / (6 g)), to nearest even, at most 448
-__device__ __forceinline__ uint32_t nv_scale_byte(float amax, float six_g) {
-  return __nv_cvt_float_to_fp8(__fdiv_rn(amax, six_g), __NV_SATFINITE, __NV_E4M3);
-}
-
 // x / T correctly rounded, given r = 1 / T correctly rounded, for |x| <= 8 T and T in
 // [2^-90, 2^100]: two residual steps (P. Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990).  q0 is within 1.5 units in the last place, q1 within one,
@@ -44,30 +39,50 @@ __device__ __forceinline__ float div_given_rcp(float x, float T, float r) {
   return fmaf(-fmaf(q1, T, -x), r, q1);
 }
 
-// four quotients by plain division (out of line: unrolled, they would crowd the instruction cache
-// of every kernel that encodes, and only blocks with an extreme scale come here)
+// four quotients by plain division, zeros for T = 0 (out of line: unrolled, they would crowd the
+// instruction cache of every kernel that encodes, and only blocks with an extreme scale come here)
 static __device__ __noinline__ float4 div4(float a, float b, float c, float d, float T) {
+  if (T == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
   return make_float4(__fdiv_rn(a, T), __fdiv_rn(b, T), __fdiv_rn(c, T), __fdiv_rn(d, T));
 }
 
+// The range of divisors that div_given_rcp takes.
+__device__ __forceinline__ bool div_range(float T) { return T >= 0x1p-90f && T <= 0x1p100f; }
+
+// NVFP4's encoder constants of a tensor: its scale g, and 6 g with the reciprocal.
+struct NvScale {
+  float g, six_g, rcp;
+  __device__ __forceinline__ explicit NvScale(float scale) {
+    g = scale;
+    six_g = 6.f * scale;
+    rcp = __frcp_rn(six_g);
+  }
+  // scale byte of a block: e4m3(amax / (6 g)), to nearest even, at most 448 (amax is cut at 1024 times
+  // 6 g, far beyond; quotients too small for an exact residual are 0 in e4m3 anyway)
+  __device__ __forceinline__ uint32_t byte(float amax) const {
+    const float q = div_range(six_g) ? div_given_rcp(fminf(amax, 1024.f * six_g), six_g, rcp) : __fdiv_rn(amax, six_g);
+    return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+  }
+};
+
 // The quotients x / T of kN values of a block under its NVFP4 scale T (zeros if T is zero).
-// amax: the block's; where its scale is cut at 448 or T is extreme, plain division.
+// amax: the block's; where its scale is cut at 448 or T is extreme, plain division, after the
+// common case so that several blocks' arithmetic can overlap.
 template <int kN>
 __device__ __forceinline__ void nv_quotients(float (&v)[kN], float T, float amax) {
-  if (T == 0.f) {
+  const float r = __frcp_rn(T);
+  float y[kN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = 0.f;
-  } else if (!(T >= 0x1p-90f && T <= 0x1p100f && amax <= 8.f * T)) {
+  for (int i = 0; i < kN; ++i) y[i] = div_given_rcp(v[i], T, r);
+  if (!(div_range(T) && amax <= 8.f * T)) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
       const float4 q = div4(v[i], v[i + 1], v[i + 2], v[i + 3], T);
-      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+      y[i] = q.x, y[i + 1] = q.y, y[i + 2] = q.z, y[i + 3] = q.w;
     }
-  } else {
-    const float r = __frcp_rn(T);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = div_given_rcp(v[i], T, r);
   }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = y[i];
 }
 
 // Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T).

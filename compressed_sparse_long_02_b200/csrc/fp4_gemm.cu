@@ -132,7 +132,7 @@ __device__ __forceinline__ int z_chunk(int tok, int c) { return tok * 16 + (c ^ 
 // lanes hold the four quarters of 128 features of one token and join their scale bytes.
 template <bool kNv>
 __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, int feat, int n_feat, int n_atoms,
-                                          const LinearParams& p, float g) {
+                                          const LinearParams& p, const NvScale& nv) {
   const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
   uint32_t codes[4], bytes = 0;
@@ -147,9 +147,9 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
   if constexpr (kNv) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t byte = nv_scale_byte(top[h], 6.f * g);
+      const uint32_t byte = nv.byte(top[h]);
       bytes |= byte << (8 * h);
-      inv[h] = e4m3_value(byte) * g;  // T
+      inv[h] = e4m3_value(byte) * nv.g;  // T
     }
   } else {
     const int E = mx_block_exponent(fmaxf(top[0], top[1]));
@@ -186,7 +186,7 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
 // Encodes four features (n_feat per row) of one token: a warp holds 128 consecutive features.
 template <bool kNv>
 __device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat, int n_feat, int n_atoms,
-                                           const LinearParams& p, float g) {
+                                           const LinearParams& p, const NvScale& nv) {
   float x[4], am = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -198,8 +198,8 @@ __device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat,
   for (int d = 1; d < kBlk / 4; d <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, d));
   uint32_t byte, codes;
   if constexpr (kNv) {
-    byte = nv_scale_byte(am, 6.f * g);
-    nv_quotients(x, e4m3_value(byte) * g, am);
+    byte = nv.byte(am);
+    nv_quotients(x, e4m3_value(byte) * nv.g, am);
     codes = e2m1x2_rn(x[0], x[1]) | e2m1x2_rn(x[2], x[3]) << 8;
   } else {
     const int E = mx_block_exponent(am);
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     constexpr int kHalf = kBN / 2;
     const int f = 32 * quarter + lane, c0 = half * kHalf;  // this lane's feature, this warp's first token of a tile
     const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
-    const float gz = kOut == kOutFp4 && kNv ? __ldg(p.gz) : 1.f;
+    const NvScale nvz(kOut == kOutFp4 && kNv ? __ldg(p.gz) : 1.f);
     const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
     if (!kPair && p.splits > 1 && warp == kOutWarp && lane == 0) {  // the bytes this CTA will receive
       int n0, g, m0;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           const int m = m0 + tok0 + i, n = n0 + 4 * lane;
           const int64_t at = static_cast<int64_t>(m) * p.ldy + static_cast<int64_t>(g) * p.N + n;
           if constexpr (kOut == kOutFp4) {
-            encode_row<kNv>(o, m, g * p.N + n, p.G * p.N, p.z_atoms, p, gz);
+            encode_row<kNv>(o, m, g * p.N + n, p.G * p.N, p.z_atoms, p, nvz);
           } else if (p.vec4 && n + 3 < p.N) {
             if constexpr (kOut == kOutBf16)
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(fp4_bf16x2(o[0], o[1]), fp4_bf16x2(o[2], o[3]));
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
               for (int j = 0; j < 4; ++j) x[j] = buf_z[z_chunk(tok, 4 * b + j)];
               const int in_tile = 64 * part + tok;
               encode_32<kNv>(x, in_tile < m_left && n0 < p.N, m0 + c0 + in_tile, g * p.N + n0 + 32 * b, p.G * p.N,
-                             p.z_atoms, p, gz);
+                             p.z_atoms, p, nvz);
             }
           }
         } else if (p.vec2) {

@@ -16,6 +16,9 @@ counters mean something, and a few GB on the device at most):
   attn_hca_64k_tail hca_attn_ex of the last 1184 raw queries of a 65536-token prefill (503-512
                     entries + the window each: the persistent tile-resident path of the 64K layer)
   proj_2k           csa_grouped_out_proj of 2048 tokens (64 heads of 512, 8 groups, R=1024, 4096)
+  proj_fp4_2k       csa_grouped_out_proj_fp4 of the same on MXFP4 weights
+  proj_fp4_32       the same of 32 tokens (a decode batch)
+  fp4_quantize_8k   csa_fp4_quantize of 8192 x 8192 bf16 (MXFP4, then NVFP4)
 """
 from __future__ import annotations
 
@@ -23,7 +26,7 @@ import argparse
 import sys
 
 CASES = ["pool_csa_64k", "pool_hca_64k", "norm_rope_q_2k", "quantize_qi_8k", "decode_128k", "attn_csa_4k",
-         "attn_hca_8k", "attn_hca_64k_tail", "proj_2k"]
+         "attn_hca_8k", "attn_hca_64k_tail", "proj_2k", "proj_fp4_2k", "proj_fp4_32", "fp4_quantize_8k"]
 
 
 def run(case: str, reps: int) -> None:
@@ -95,6 +98,15 @@ def run(case: str, reps: int) -> None:
         ps = synth.PROJ["csa_prefill_8k"]
         d = synth.proj_inputs_torch(ps, dev, T=2048)
         fn = lambda: B.csa_grouped_out_proj(d["o"], d["A"], d["Bm"])
+    elif case in ("proj_fp4_2k", "proj_fp4_32"):
+        ps = synth.PROJ["csa_prefill_8k"]
+        d = synth.proj_inputs_torch(ps, dev, T=2048 if case == "proj_fp4_2k" else 32)
+        A, Bm = B.csa_fp4_quantize(d["A"].reshape(ps.G * ps.R, -1)), B.csa_fp4_quantize(d["Bm"])
+        fn = lambda: B.csa_grouped_out_proj_fp4(d["o"], A, Bm, groups=ps.G)
+    elif case == "fp4_quantize_8k":
+        x = torch.randn((8192, 8192), device=dev).to(torch.bfloat16)
+        scale = (x.float().abs().amax() / 2688).reshape(1)
+        fn = lambda: (B.csa_fp4_quantize(x), B.csa_fp4_quantize(x, fmt="nvfp4", tensor_scale=scale))
     else:
         raise SystemExit(f"unknown case {case}; one of {', '.join(CASES)}")
     for _ in range(reps):
