@@ -56,6 +56,9 @@ constexpr int kHintWarp = 2;         // asks for the first tile's weights in L2
 constexpr int kSfWarp = 4;           // first of the four scale warps
 constexpr int kOutWarp = 8;          // first of the eight result warps
 
+constexpr int kPart = 32;
+constexpr uint32_t kPartBytes = kPart * kTileN * 2;  // see part_at
+
 enum Out { kOutF32, kOutBf16, kOutFp4 };
 
 template <bool kNv, int kBN, int kOut>
@@ -69,8 +72,8 @@ struct Shape {
   static constexpr uint32_t kBytesX = kRowsX * kSlabBytes;
   static constexpr uint32_t kBytesSf = 512 * kAtoms * (1 + kRowBlocks);
   static constexpr uint32_t kStage = kBytesW + kBytesX + kBytesSf;
-  // lone CTAs: float32 partials, all CTAs', of this CTA's tokens; pairs: 2 x 64 tokens to encode
-  static constexpr uint32_t kRecv = kPair ? (kOut == kOutFp4 ? 2 * 64 * kTileN * 2 : 0) : kBN * kTileN * 4;
+  // lone CTAs: float32 partials, all CTAs', of this CTA's tokens; pairs: two parts of each half
+  static constexpr uint32_t kRecv = kPair ? (kOut == kOutF32 ? 0 : 4 * kPart * kTileN * 2) : kBN * kTileN * 4;
   // Up to 64 tokens (decode) two CTAs share an SM: the next launch's CTAs set up, and wait for
   // their grid, next to the running ones.
   static constexpr int kMinBlocks = kBN <= 64 ? 2 : 1;
@@ -100,7 +103,8 @@ struct LinearParams {
   const float* gw;
   void* y;
   int64_t ldy;
-  int vec2, vec4;         // rows of y allow stores of 2 or 4 features
+  int tma_y;              // y has a tensor map (pairs, bf16)
+  int vec4;               // rows of y allow stores of 4 features
   uint8_t* z_packed;      // kOutFp4: codes [M, G N / 2], scales, tensor scale
   uint8_t* z_scale;
   const float* gz;
@@ -123,10 +127,13 @@ __device__ __forceinline__ int64_t scale_at(int m, int blk, int n_atoms) {
   return fp4_atom_offset(m / 128, blk / 4, n_atoms) + (m % 32) * 16 + (m % 128) / 32 * 4 + blk % 4;
 }
 
-// The pair's encoding of 64 tokens x 128 features goes through shared memory, where a row of 128
-// bf16 features is sixteen 16-byte chunks, placed so that both a warp's writes (32 features of two
-// tokens) and its reads (32 features of each of eight tokens per chunk) spread over the banks.
-__device__ __forceinline__ int z_chunk(int tok, int c) { return tok * 16 + (c ^ ((c >> 3) & 1) ^ ((tok & 1) << 1)); }
+// A pair's results pass through shared memory in parts of 32 tokens x 128 bf16 features: two
+// blocks of 64 features, each [32 tokens][128 bytes] with the 16-byte chunks swizzled by the token
+// (SWIZZLE_128B).  The accumulator's 8 x 8 pieces go in transposed (stmatrix), without bank
+// conflicts; a TMA store, or the encoder, takes whole rows out.
+__device__ __forceinline__ uint32_t part_at(int tok, int chunk) {  // chunk: 8 features, 0..15
+  return static_cast<uint32_t>((chunk >> 3) * kPart * 128 + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4));
+}
 
 // Encodes 32 consecutive features (feat, a multiple of 32) of one bf16 token; four neighbouring
 // lanes hold the four quarters of 128 features of one token and join their scale bytes.
@@ -215,7 +222,7 @@ template <bool kNv, int kBN, int kOut>
 __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
-                      const LinearParams p) {
+                      const __grid_constant__ CUtensorMap tm_y, const LinearParams p) {
   using S = Shape<kNv, kBN, kOut>;
   constexpr bool kPair = S::kPair;
   extern __shared__ uint8_t smem_raw[];
@@ -574,69 +581,76 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           }
         }
       } else {
-        // the warp's whole share rounded to bf16 in registers, then stored while the next tile runs
-        uint32_t v[kHalf / 2];
+        // the warp's whole share rounded to bf16 in registers: 8 x 8 pieces, v[i][m] of tokens 8i.. and
+        // features 8m.., which leave part by part while the next tile runs
+        uint32_t v[kHalf / 8][4];
 #pragma unroll
         for (int c = 0; c < kHalf; c += 32) {
-          uint32_t u[32];
-          tmem_ld16(src + c, u);
-          tmem_ld16(src + c + 16, u + 16);
+          uint32_t u[2][16];
+          tmem_ld_16x256b_x4(src + c, u[0]);
+          tmem_ld_16x256b_x4(src + (16u << 16) + c, u[1]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            v[c / 2 + i] = fp4_bf16x2(__uint_as_float(u[2 * i]) * alpha, __uint_as_float(u[2 * i + 1]) * alpha);
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              v[c / 8 + i][m] = fp4_bf16x2(__uint_as_float(u[m / 2][4 * i + 2 * (m & 1)]) * alpha,
+                                           __uint_as_float(u[m / 2][4 * i + 2 * (m & 1) + 1]) * alpha);
+          }
         }
         release();
-        const int n = n0 + f;
-        const int64_t at = static_cast<int64_t>(m0 + c0) * p.ldy + static_cast<int64_t>(g) * p.N + n;
-        if constexpr (kOut == kOutFp4) {
-          // 64 tokens at a time among the four warps of this half, whose lanes hold all 128 features
-          uint4* buf_z = reinterpret_cast<uint4*>(recv) + half * 64 * 16;
-          uint32_t* buf_w = reinterpret_cast<uint32_t*>(buf_z);
-          const int odd = lane & 1, id = quarter * 32 + lane;
+        // the four warps of this half alternate between its two part buffers, one barrier a part: who
+        // passes the next part's barrier has left this one's buffer
+        const int id = quarter * 32 + lane;
 #pragma unroll
-          for (int part = 0; part < kHalf / 64; ++part) {
-            named_bar_sync(1 + half, 128);  // the last readers are done
+        for (int part = 0; part < kHalf / kPart; ++part) {
+          uint8_t* buf_z = reinterpret_cast<uint8_t*>(recv) + (2 * half + (part & 1)) * kPartBytes;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const uint32_t x = v[32 * part + i], o = __shfl_xor_sync(0xffffffffu, x, 1);
-              buf_w[4 * z_chunk(2 * i + odd, f >> 3) + ((f >> 1) & 3)] = odd ? __byte_perm(o, x, 0x7632) : __byte_perm(x, o, 0x5410);
-            }
+          for (int i = 0; i < kPart / 8; ++i) {
+            const uint32_t* q = v[part * (kPart / 8) + i];
+            stmatrix_x4_trans(smem_u32(buf_z) + part_at(8 * i + (lane & 7), 4 * quarter + (lane >> 3)), q[0], q[1], q[2], q[3]);
+          }
+          const int left = m_left - part * kPart, m = m0 + c0 + part * kPart;  // tokens of this part
+          if constexpr (kOut == kOutFp4) {
             named_bar_sync(1 + half, 128);
+            const int tok = id / 4, b = id % 4;
+            uint4 x[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int tok = u * 32 + id / 4, b = id % 4;
-              uint4 x[4];
+            for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(buf_z + part_at(tok, 4 * b + j));
+            encode_32<kNv>(x, tok < left && n0 < p.N, m + tok, g * p.N + n0 + 32 * b, p.G * p.N, p.z_atoms, p, nvz);
+          } else if (p.tma_y) {
+            fence_proxy_async_smem();
+            if (id == 0) bulk_wait_read();  // the other buffer's store has read it
+            named_bar_sync(1 + half, 128);
+            if (id == 0 && left > 0) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) x[j] = buf_z[z_chunk(tok, 4 * b + j)];
-              const int in_tile = 64 * part + tok;
-              encode_32<kNv>(x, in_tile < m_left && n0 < p.N, m0 + c0 + in_tile, g * p.N + n0 + 32 * b, p.G * p.N,
-                             p.z_atoms, p, nvz);
+              for (int h = 0; h < 2; ++h)
+                if (n0 + 64 * h < p.N) tma_store_2d(&tm_y, smem_u32(buf_z) + h * kPart * 128, g * p.N + n0 + 64 * h, m);
+              bulk_commit();
             }
-          }
-        } else if (p.vec2) {
-          // lanes 2i and 2i + 1 trade: the even lane stores both features of the even token, the odd
-          // lane those of the odd token, four bytes each
-          const int odd = lane & 1;
-          char* y = static_cast<char*>(p.y) + 2 * (at - odd + odd * p.ldy);
-          const int64_t step_y = 4 * p.ldy;
-          const bool in = n - odd < p.N;
+          } else {  // rows that no tensor map can describe: a token per warp at a time
+            named_bar_sync(1 + half, 128);
+            uint16_t* y = static_cast<uint16_t*>(p.y) + static_cast<int64_t>(m) * p.ldy + static_cast<int64_t>(g) * p.N + n0;
 #pragma unroll
-          for (int i = 0; i < kHalf / 2; ++i) {
-            const uint32_t o = __shfl_xor_sync(0xffffffffu, v[i], 1);
-            const uint32_t w = odd ? __byte_perm(o, v[i], 0x7632) : __byte_perm(v[i], o, 0x5410);
-            if (in && 2 * i + odd < m_left) *reinterpret_cast<uint32_t*>(y) = w;
-            y += step_y;
-          }
-        } else if (n < p.N) {
-          uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+            for (int k = 0; k < kPart / 4; ++k) {
+              const int tok = quarter + 4 * k;
+              if (tok >= left) break;
+              uint16_t* row = y + tok * p.ldy;
+              if (p.vec4) {
+                if (n0 + 4 * lane < p.N)
+                  reinterpret_cast<uint2*>(row)[lane] = *reinterpret_cast<const uint2*>(buf_z + part_at(tok, lane >> 1) + 8 * (lane & 1));
+              } else {
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            if (i < m_left) *y = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
-            y += p.ldy;
+                for (int e = lane; e < kTileN; e += 32)
+                  if (n0 + e < p.N) row[e] = *reinterpret_cast<const uint16_t*>(buf_z + part_at(tok, e >> 3) + 2 * (e & 7));
+              }
+            }
           }
         }
       }
+    }
+    if constexpr (kPair && kOut == kOutBf16) {
+      if (quarter == 0 && lane == 0) bulk_wait();  // nothing may read this CTA's shared memory after it is gone
     }
   }
 
@@ -685,13 +699,15 @@ template <bool kNv, int kBN, int kOut>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cudaStream_t s) {
   using Sh = Shape<kNv, kBN, kOut>;
   static int smem_set[64], pairs[64];
-  CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
+  CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y = {};
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
   if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
       !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
     return cudaErrorInvalidValue;
+  if (Sh::kPair && kOut == kOutBf16 && a.N % 8 == 0 && a.ldy % 8 == 0)
+    p.tma_y = encode_2d_bf16(&tm_y, a.y, w_rows, a.M, a.ldy, kPart);
   p.m_blocks = (a.M + kBN - 1) / kBN;
   p.n_blocks = (a.N + kTileN * Sh::kCtas - 1) / (kTileN * Sh::kCtas);
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks * a.G;
@@ -704,13 +720,13 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
   if constexpr (Sh::kPair) {
     p.splits = 1;
     const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
-    return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, p);
+    return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
   } else {
     p.splits = splits;
     const int64_t clusters = splits > 1 ? tiles : std::min<int64_t>(tiles, num_sms() * Sh::kMinBlocks);
     const dim3 grid(static_cast<unsigned>(clusters * p.splits));
-    if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, p);
-    return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, p);
+    if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
+    return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
   }
 }
 
@@ -775,7 +791,6 @@ cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s) {
   p.gw = a.gw;
   p.y = a.y;
   p.ldy = a.ldy;
-  p.vec2 = a.N % 2 == 0 && a.ldy % 2 == 0;
   p.vec4 = a.N % 4 == 0 && a.ldy % 4 == 0;
   p.z_packed = a.z_packed;
   p.z_scale = a.z_scale;
