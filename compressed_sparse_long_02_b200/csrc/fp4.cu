@@ -137,11 +137,14 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(nv, packed, (row0 + 32 * i) * p.cols + col, in);
     } else {  // the last row block: one row at a time, so that rows that only pad it cost nothing
+      RT rt;
+      rt.load(x, row0 * p.ld + col, in && row0 < p.rows);
 #pragma unroll 1
       for (int64_t row = row0; row < p.rows; row += 32) {
-        RT rt;
-        rt.load(x, row * p.ld + col, in);
+        RT next;
+        next.load(x, (row + 32) * p.ld + col, in && row + 32 < p.rows);
         const uint32_t v = rt.encode(nv, packed, row * p.cols + col, in);
+        rt = next;
         const int i = static_cast<int>((row - row0) / 32);
         w[0] = i == 0 ? v : w[0];
         w[1] = i == 1 ? v : w[1];

@@ -74,9 +74,9 @@ struct Shape {
   static constexpr uint32_t kStage = kBytesW + kBytesX + kBytesSf;
   // lone CTAs: float32 partials, all CTAs', of this CTA's tokens; pairs: two parts of each half
   static constexpr uint32_t kRecv = kPair ? (kOut == kOutF32 ? 0 : 4 * kPart * kTileN * 2) : kBN * kTileN * 4;
-  // Up to 64 tokens (decode) two CTAs share an SM: the next launch's CTAs set up, and wait for
+  // Up to 32 tokens (decode) two CTAs share an SM: the next launch's CTAs set up, and wait for
   // their grid, next to the running ones.
-  static constexpr int kMinBlocks = kBN <= 64 ? 2 : 1;
+  static constexpr int kMinBlocks = kBN <= 32 ? 2 : 1;
   static constexpr int kFit = static_cast<int>(((kMinBlocks == 2 ? 111u : 225u) * 1024u - kRecv) / kStage);
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kRecv + 512;
@@ -99,6 +99,7 @@ struct LinearParams {
   int n_blocks, m_blocks, tiles, splits;
   int x_atoms, w_atoms;   // scale atoms per row block of X and W
   int x_group_atoms;      // atoms of one group's K columns of X
+  int box_rows;           // rows that a slab's two loads bring in, W's and X's
   const float* gx;
   const float* gw;
   void* y;
@@ -331,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             ok = false;
             break;
           }
-          // codes past K, rows past the ends and scale blocks past the end read as zeros or belong to
-          // columns that no MMA step covers, so every slab counts the same bytes
+          // codes past K, a last tile's rows past the ends and scale blocks past the end read as zeros or
+          // belong to columns that no MMA step covers, so every slab counts the same bytes
           const int sf0 = sl * S::kAtoms;
           const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
           const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           tma_load_2d(ds, &tm_ws, &sf_full[st], 0, w_sf + sf0);
           for (int rb = 0; rb < S::kRowBlocks; ++rb)
             tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &sf_full[st], 0, x_sf + rb * p.x_atoms + sf0);
-          if (leader) mbar_arrive_expect_tx(&full[st], (S::kBytesW + S::kBytesX) * S::kCtas);
+          if (leader) mbar_arrive_expect_tx(&full[st], p.box_rows * kSlabBytes * S::kCtas);
           if constexpr (kPair) {
             const uint32_t bar = dsmem_map(&full[st], 0);
             tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
@@ -672,37 +673,38 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   }
 }
 
-// Clusters of two that the device holds at once (asked for once per kernel and device).
+// Clusters of `size` CTAs that the device holds at once; fewer than its SMs would give, since a
+// cluster stays within one GPC.
 template <typename K>
-int resident_pairs(K k, size_t smem, int* cache) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (cache[dev] == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / 2 * 2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    cache[dev] = cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : num_sms() / 2;
-  }
-  return cache[dev];
+int resident_clusters(K k, size_t smem, int size) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / size * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : num_sms() / size;
 }
 
 template <bool kNv, int kBN, int kOut>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cudaStream_t s) {
   using Sh = Shape<kNv, kBN, kOut>;
-  static int smem_set[64], pairs[64];
+  static int smem_set[64], resident[64];  // pairs: what runs at once, per device
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y = {};
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
-  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  // A box is no higher than its matrix: rows past the end cost a load as much as rows do (4096 x 14 x
+  // 2048: 15.4 us with boxes of 128 rows of W, 6.9 us for 128 features).  What the missing rows of
+  // shared memory hold reaches only results that are not stored.
+  const int x_box = std::min(a.M, Sh::kRowsX), w_box = static_cast<int>(std::min<uint64_t>(w_rows, kTileN));
+  p.box_rows = x_box + w_box;
+  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, x_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, w_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
       !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
     return cudaErrorInvalidValue;
@@ -719,7 +721,10 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
   const dim3 block(kThreads);
   if constexpr (Sh::kPair) {
     p.splits = 1;
-    const int64_t n = std::min<int64_t>(tiles, resident_pairs(k, Sh::kSmem, pairs));
+    int dev = 0;
+    cudaGetDevice(&dev);  // 0..63: set_dyn_smem accepted it
+    if (resident[dev] == 0) resident[dev] = resident_clusters(k, Sh::kSmem, 2);
+    const int64_t n = std::min<int64_t>(tiles, resident[dev]);
     return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
   } else {
     p.splits = splits;
@@ -731,42 +736,74 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
 }
 
 // Tokens per tile and CTAs per tile (a split of K), by the time that each choice would take in
-// nanoseconds beyond what all have in common.  Measured on one B200 (us, 32 / 64 / 128 tokens a
-// tile at their best splits, and pairs): 1 x 4096 x 8192 6.9 / 7.0 / 7.9 / 17; 64 x 4096 x 8192
-// 9.6 / 8.8 / 10.1 / 18; 256 x 4096 x 8192 20 / 14.5 / 14.7 / 18.5; 512 x 4096 x 8192 34 / 21 /
-// 18.7 / 18.7; 600 x 256 x 512, 4 groups, 4.6 / 4.7 / 5.5 / 6.4.  The terms, from the same runs:
-//   a slab of a lone CTA 430 ns, 530 with two on an SM (the latency of its loads, not their
-//   bytes); a slab of a pair 450, and 2000 for its results, which nothing else covers;
-//   a split 400 plus 20 a token (35 at 128 a tile) for the exchanged sums, on a shared SM twice
-//   that and 1500 for a set-up that no longer hides behind the launch before;
+// nanoseconds beyond what all have in common.  Measured on one B200 (us; 32 / 64 / 128 tokens a
+// tile at their best splits, and pairs): 1 x 4096 x 8192 6.5 / 7.6 / 8.7 / 15; 64 x 4096 x 8192
+// 9.5 / 9.1 / 10 / 15; 256 x 4096 x 8192 19 / 17 / 14.5 / 16; 512 x 4096 x 8192 32 / 29 / 18.5 /
+// 16.4; 600 x 256 x 512, 4 groups, 4.5 / 4.5 / 5.4 / 5.6.  The terms, from the same runs:
+//   a slab of a lone CTA 370, 400, 430 by its width (what one SM loads), 480 with two on an SM;
+//   a slab of a pair 380, and 1500 for the hand-over between tiles (2500 where rows of y have no
+//   tensor map);
+//   a split 400 plus 30 a token for the exchanged sums (35 at 64 and 128 tokens, and 400 for a
+//   set-up that no launch before it hides; twice the 30 and 1500 on a shared SM);
 //   unsplit results 10 a token.
 // In batch-invariant mode K is never split, so a row's sums run over K in one order whatever the
 // number of rows.
 struct Choice {
   int tokens, splits;
 };
-Choice choose(int M, int N, int K, int G) {
-  const int64_t sms = num_sms(), slabs = (K + kSlab - 1) / kSlab;
-  const int64_t rows = static_cast<int64_t>(G) * ((N + kTileN - 1) / kTileN);
-  const int64_t pairs = static_cast<int64_t>(G) * ((N + 2 * kTileN - 1) / (2 * kTileN)) * ((M + 255) / 256);
+// resident[wide][i]: clusters of 2^i lone CTAs that run at once, 32 tokens a tile or wider
+Choice choose(const Fp4LinearArgs& a, const int (&resident)[2][4]) {
+  const int64_t slabs = (a.K + kSlab - 1) / kSlab, sms = num_sms();
+  const int64_t rows = static_cast<int64_t>(a.G) * ((a.N + kTileN - 1) / kTileN);
+  const int64_t pairs = static_cast<int64_t>(a.G) * ((a.N + 2 * kTileN - 1) / (2 * kTileN)) * ((a.M + 255) / 256);
+  const bool tma_y = a.z_packed != nullptr || (a.out_bf16 && a.N % 8 == 0 && a.ldy % 8 == 0);
   Choice best{256, 1};
-  int64_t cost = (pairs + sms / 2 - 1) / (sms / 2) * (slabs * 450 + 2000);
-  for (int bn = 32; bn <= 128; bn *= 2) {
-    const int64_t tiles = rows * ((M + bn - 1) / bn), room = bn <= 64 ? 2 * sms : sms, tok = std::min(M, bn);
-    for (int sp = 1; sp <= (batch_invariant() ? 1 : 8) && sp <= slabs; sp *= 2) {
-      const int64_t ctas = tiles * sp, shared = ctas > sms && bn <= 64 ? 1 : 0;
-      if (sp > 1 && ctas > room) break;
-      const int64_t ends = sp > 1 ? 400 + (bn == 128 ? 35 : 20 * (1 + shared)) * tok + 1500 * shared : 10 * (1 + shared) * tok;
-      const int64_t c = (ctas + room - 1) / room * ((slabs + sp - 1) / sp * (shared ? 530 : 430) + ends);
-      if (c < cost) cost = c, best = Choice{bn, sp};
+  int64_t cost = (pairs + sms / 2 - 1) / (sms / 2) * (slabs * 380 + (tma_y ? 1500 : 2500));
+  for (int i = 0; i < 3; ++i) {
+    const int bn = 32 << i;
+    const int64_t tiles = rows * ((a.M + bn - 1) / bn), tok = std::min(a.M, bn);
+    for (int j = 0; j < (batch_invariant() ? 1 : 4) && (1 << j) <= slabs; ++j) {
+      const int64_t ctas = tiles << j, shared = bn == 32 && ctas > sms ? 1 : 0, room = resident[i > 0][j];
+      if (j > 0 && tiles > room) break;
+      const int64_t slab = bn == 32 ? (shared ? 480 : 370) : (bn == 64 ? 400 : 430);
+      const int64_t ends = j == 0 ? 10 * (1 + shared) * tok
+                                  : 400 + (bn == 32 ? 30 * (1 + shared) * tok + 1500 * shared : 35 * tok + 400);
+      const int64_t c = (tiles + room - 1) / room * (((slabs + (1 << j) - 1) >> j) * slab + ends);
+      if (c < cost) cost = c, best = Choice{bn, 1 << j};
     }
   }
   return best;
 }
 
+// The table of choose() for a format and a kind of result, asked for once per device.
+template <bool kNv, int kOut>
+cudaError_t lone_residents(const int (**out)[2][4]) {
+  static int table[64][2][4];
+  static int smem_set[2][64];
+  int dev = 0;
+  const cudaError_t g = cudaGetDevice(&dev);
+  if (g != cudaSuccess) return g;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  *out = &table[dev];
+  if (table[dev][1][3] != 0) return cudaSuccess;
+  const auto narrow = fp4_linear_kernel<kNv, 32, kOut>, wide = fp4_linear_kernel<kNv, 128, kOut>;
+  constexpr size_t narrow_smem = Shape<kNv, 32, kOut>::kSmem, wide_smem = Shape<kNv, 128, kOut>::kSmem;
+  cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(narrow), narrow_smem, smem_set[0]);
+  if (e == cudaSuccess) e = set_dyn_smem(reinterpret_cast<const void*>(wide), wide_smem, smem_set[1]);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < 4; ++i) {
+    table[dev][0][i] = resident_clusters(narrow, narrow_smem, 1 << i);
+    table[dev][1][i] = resident_clusters(wide, wide_smem, 1 << i);
+  }
+  return cudaSuccess;
+}
+
 template <bool kNv, int kOut>
 cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
-  const Choice c = choose(a.M, a.N, a.K, a.G);
+  const int(*resident)[2][4] = nullptr;
+  const cudaError_t e = lone_residents<kNv, kOut>(&resident);
+  if (e != cudaSuccess) return e;
+  const Choice c = choose(a, *resident);
   switch (c.tokens) {
     case 32: return launch_tile<kNv, 32, kOut>(a, p, c.splits, s);
     case 64: return launch_tile<kNv, 64, kOut>(a, p, c.splits, s);
