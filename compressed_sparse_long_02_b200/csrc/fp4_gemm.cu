@@ -99,7 +99,6 @@ struct LinearParams {
   int n_blocks, m_blocks, tiles, splits;
   int x_atoms, w_atoms;   // scale atoms per row block of X and W
   int x_group_atoms;      // atoms of one group's K columns of X
-  int box_rows;           // rows that a slab's two loads bring in, W's and X's
   const float* gx;
   const float* gw;
   void* y;
@@ -222,6 +221,7 @@ __device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat,
 template <bool kNv, int kBN, int kOut>
 __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_xt, const __grid_constant__ CUtensorMap tm_wt,
                       const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                       const __grid_constant__ CUtensorMap tm_y, const LinearParams p) {
   using S = Shape<kNv, kBN, kOut>;
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     int n0, g, m0;
     tile(first, n0, g, m0);
     const int w_row = g * p.N + n0, sl = slab0 + lane;
-    if (sl < slab1) {
-      tma_prefetch_2d(&tm_w, sl * kSlabBytes, w_row);
+    if (sl < slab1 && n0 < p.N) {
+      tma_prefetch_2d(n0 + kTileN <= p.N ? &tm_w : &tm_wt, sl * kSlabBytes, w_row);
       tma_prefetch_2d(&tm_ws, 0, w_row / 128 * p.w_atoms + sl * S::kAtoms);
     }
   }
@@ -325,6 +325,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         tile(t, n0, g, m0);
         const int w_row = g * p.N + n0;
         const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);  // a pair's MMA takes half of its tokens from each CTA
+        // Only rows that exist are loaded (the maps tm_xt, tm_wt have the boxes of the last rows): rows
+        // past the end cost a load more than rows do -- 4096 x 14 x 2048 took 15.4 us with boxes of 128
+        // rows of W, 6.4 us with 14.  What the missing rows of shared memory hold reaches only results
+        // that are not stored.
+        auto rows_of = [](int total, int at, int box) { return max(0, min(box, total - at)); };
+        const int w_rows = rows_of(p.N, n0, kTileN), x_rows = rows_of(p.M, x_row, S::kRowsX);
+        int rows = w_rows + x_rows;
+        if constexpr (kPair) rows += rows_of(p.N, n0 + kTileN, kTileN) + rows_of(p.M, x_row + S::kRowsX, S::kRowsX);  // the leader's count
+        const CUtensorMap* map_w = w_rows == kTileN ? &tm_w : &tm_wt;
+        const CUtensorMap* map_x = x_rows == S::kRowsX ? &tm_x : &tm_xt;
         const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
         for (int sl = slab0; sl < slab1; ++sl, ++j) {
           const int st = j % S::kStages;
@@ -332,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             ok = false;
             break;
           }
-          // codes past K, a last tile's rows past the ends and scale blocks past the end read as zeros or
-          // belong to columns that no MMA step covers, so every slab counts the same bytes
+          // codes past K and scale blocks past the end read as zeros or belong to columns that no MMA step
+          // covers, so every slab of a tile counts the same bytes
           const int sf0 = sl * S::kAtoms;
           const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
           const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
@@ -341,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           tma_load_2d(ds, &tm_ws, &sf_full[st], 0, w_sf + sf0);
           for (int rb = 0; rb < S::kRowBlocks; ++rb)
             tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &sf_full[st], 0, x_sf + rb * p.x_atoms + sf0);
-          if (leader) mbar_arrive_expect_tx(&full[st], p.box_rows * kSlabBytes * S::kCtas);
+          if (leader) mbar_arrive_expect_tx(&full[st], rows * kSlabBytes);
           if constexpr (kPair) {
             const uint32_t bar = dsmem_map(&full[st], 0);
-            tma_load_2d_pair(dw, &tm_w, bar, sl * kSlabBytes, w_row);
-            tma_load_2d_pair(dx, &tm_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
+            if (w_rows > 0) tma_load_2d_pair(dw, map_w, bar, sl * kSlabBytes, w_row);
+            if (x_rows > 0) tma_load_2d_pair(dx, map_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
           } else {
-            tma_load_2d(dw, &tm_w, &full[st], sl * kSlabBytes, w_row);
-            tma_load_2d(dx, &tm_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
+            tma_load_2d(dw, map_w, &full[st], sl * kSlabBytes, w_row);
+            tma_load_2d(dx, map_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
           }
         }
       }
@@ -696,15 +706,13 @@ template <bool kNv, int kBN, int kOut>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cudaStream_t s) {
   using Sh = Shape<kNv, kBN, kOut>;
   static int smem_set[64], resident[64];  // pairs: what runs at once, per device
-  CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y = {};
+  CUtensorMap tm_x, tm_w, tm_xt = {}, tm_wt = {}, tm_xs, tm_ws, tm_y = {};
   const uint64_t xb = static_cast<uint64_t>(a.G) * a.K / 2, wb = a.K / 2, w_rows = static_cast<uint64_t>(a.G) * a.N;
-  // A box is no higher than its matrix: rows past the end cost a load as much as rows do (4096 x 14 x
-  // 2048: 15.4 us with boxes of 128 rows of W, 6.9 us for 128 features).  What the missing rows of
-  // shared memory hold reaches only results that are not stored.
-  const int x_box = std::min(a.M, Sh::kRowsX), w_box = static_cast<int>(std::min<uint64_t>(w_rows, kTileN));
-  p.box_rows = x_box + w_box;
-  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, x_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, w_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const uint32_t x_tail = a.M % Sh::kRowsX, w_tail = a.N % kTileN;  // (groups are whole tiles)
+  if (!encode_2d_u8(&tm_x, a.x_packed, xb, a.M, kSlabBytes, Sh::kRowsX, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d_u8(&tm_w, a.w_packed, wb, w_rows, kSlabBytes, kTileN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (x_tail != 0 && !encode_2d_u8(&tm_xt, a.x_packed, xb, a.M, kSlabBytes, x_tail, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (w_tail != 0 && !encode_2d_u8(&tm_wt, a.w_packed, wb, w_rows, kSlabBytes, w_tail, CU_TENSOR_MAP_SWIZZLE_128B)) ||
       !encode_blocks_512(&tm_xs, a.x_scale, static_cast<uint64_t>((a.M + 127) / 128) * p.x_atoms, Sh::kAtoms) ||
       !encode_blocks_512(&tm_ws, a.w_scale, (w_rows + 127) / 128 * p.w_atoms, Sh::kAtoms))
     return cudaErrorInvalidValue;
@@ -725,13 +733,13 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
     cudaGetDevice(&dev);  // 0..63: set_dyn_smem accepted it
     if (resident[dev] == 0) resident[dev] = resident_clusters(k, Sh::kSmem, 2);
     const int64_t n = std::min<int64_t>(tiles, resident[dev]);
-    return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
+    return launch_pdl_cluster(k, dim3(static_cast<unsigned>(2 * n)), block, Sh::kSmem, 2, s, tm_x, tm_w, tm_xt, tm_wt, tm_xs, tm_ws, tm_y, p);
   } else {
     p.splits = splits;
     const int64_t clusters = splits > 1 ? tiles : std::min<int64_t>(tiles, num_sms() * Sh::kMinBlocks);
     const dim3 grid(static_cast<unsigned>(clusters * p.splits));
-    if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
-    return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xs, tm_ws, tm_y, p);
+    if (p.splits == 1) return launch_pdl(k, grid, block, Sh::kSmem, s, tm_x, tm_w, tm_xt, tm_wt, tm_xs, tm_ws, tm_y, p);
+    return launch_pdl_cluster(k, grid, block, Sh::kSmem, p.splits, s, tm_x, tm_w, tm_xt, tm_wt, tm_xs, tm_ws, tm_y, p);
   }
 }
 
