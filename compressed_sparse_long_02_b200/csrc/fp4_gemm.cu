@@ -21,10 +21,13 @@
 //
 // Pairs (kBN = 256): the two CTAs of a cluster form one tile of 256 features x 256 tokens
 // (cta_group::2).  Each loads its own 128 features and half of the tokens, so a slab costs an SM
-// 35 KB instead of the 51 KB of a lone 128 x 256 tile; what feeds the FP4 MMAs is L2, at about
-// 83 GB/s per SM, so that ratio is the kernel's speed.  The 256 accumulator columns leave no room
-// for a second accumulator next to the scales: the result warps first read the tile into
-// registers, release it, and convert and store while the next tile's MMAs run.
+// 35 KB instead of the 51 KB of a lone 128 x 256 tile (8192 x 4096 x 8192 MXFP4: 198 us with lone
+// tiles, 139 with pairs, 98 with the scales and the MMA issue as described here).  The 256
+// accumulator columns leave no room for a second accumulator next to the scales: the result warps
+// first read the tile into registers, release it, and convert and store while the next tile's MMAs
+// run.  A slab then takes 0.38 us: 87 GB/s per SM from L2, 0.27 us of MMAs.  Back to back for
+// seconds the power limit holds the clock near 1.6 GHz and the same product takes 115 us.  Pairs
+// of 384 tokens (44 KB for 1.5 times the work) measured the same.
 //
 // Lone CTAs (kBN <= 128): with few tiles the K axis is split over the S CTAs of a cluster.  Each
 // CTA sends every other its float32 partial sums of that CTA's tokens (asynchronous stores into
@@ -287,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   const int slabs = (p.K + kSlab - 1) / kSlab;
   const int slab0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(slabs) * rank / p.splits);
   const int slab1 = kPair ? slabs : static_cast<int>(static_cast<int64_t>(slabs) * (rank + 1) / p.splits);
-  // tile t: features [n0, n0 + 128) of group g (this CTA's), tokens [m0, m0 + kBN); feature blocks
-  // run fastest, so the CTAs at work share a few token blocks and all weights of L2
   auto commit = [](uint64_t* bar) {
     if constexpr (kPair)
       tc_commit_pair(bar);
     else
       tc_commit(bar);
   };
+  // tile t: features [n0, n0 + 128) of group g (this CTA's), tokens [m0, m0 + kBN); feature blocks
+  // run fastest, so the CTAs at work share a few token blocks and all weights of L2
   auto tile = [&](int t, int& n0, int& g, int& m0) {
     const int nb = t % p.n_blocks, mg = t / p.n_blocks;
     n0 = (nb * S::kCtas + (kPair ? rank : 0)) * kTileN;
@@ -314,132 +317,132 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   griddep_enter();
 
   if (warp < kSfWarp) {
-   regs_dec<S::kRegsIssue>();
-   if (warp == 0) {
-    // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      int j = 0;
-      bool ok = true;
-      for (int t = first; ok && t < p.tiles; t += step) {
-        int n0, g, m0;
-        tile(t, n0, g, m0);
-        const int w_row = g * p.N + n0;
-        const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);  // a pair's MMA takes half of its tokens from each CTA
-        // Only rows that exist are loaded (the maps tm_xt, tm_wt have the boxes of the last rows): rows
-        // past the end cost a load more than rows do -- 4096 x 14 x 2048 took 15.4 us with boxes of 128
-        // rows of W, 6.4 us with 14.  What the missing rows of shared memory hold reaches only results
-        // that are not stored.
-        auto rows_of = [](int total, int at, int box) { return max(0, min(box, total - at)); };
-        const int w_rows = rows_of(p.N, n0, kTileN), x_rows = rows_of(p.M, x_row, S::kRowsX);
-        int rows = w_rows + x_rows;
-        if constexpr (kPair) rows += rows_of(p.N, n0 + kTileN, kTileN) + rows_of(p.M, x_row + S::kRowsX, S::kRowsX);  // the leader's count
-        const CUtensorMap* map_w = w_rows == kTileN ? &tm_w : &tm_wt;
-        const CUtensorMap* map_x = x_rows == S::kRowsX ? &tm_x : &tm_xt;
-        const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
-        for (int sl = slab0; sl < slab1; ++sl, ++j) {
-          const int st = j % S::kStages;
-          if (!mbar_wait(&empty[st], ((j / S::kStages) & 1) ^ 1, p.err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          // codes past K and scale blocks past the end read as zeros or belong to columns that no MMA step
-          // covers, so every slab of a tile counts the same bytes
-          const int sf0 = sl * S::kAtoms;
-          const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
-          const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
-          mbar_arrive_expect_tx(&sf_full[st], S::kBytesSf);
-          tma_load_2d(ds, &tm_ws, &sf_full[st], 0, w_sf + sf0);
-          for (int rb = 0; rb < S::kRowBlocks; ++rb)
-            tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &sf_full[st], 0, x_sf + rb * p.x_atoms + sf0);
-          if (leader) mbar_arrive_expect_tx(&full[st], rows * kSlabBytes);
-          if constexpr (kPair) {
-            const uint32_t bar = dsmem_map(&full[st], 0);
-            if (w_rows > 0) tma_load_2d_pair(dw, map_w, bar, sl * kSlabBytes, w_row);
-            if (x_rows > 0) tma_load_2d_pair(dx, map_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
-          } else {
-            tma_load_2d(dw, map_w, &full[st], sl * kSlabBytes, w_row);
-            tma_load_2d(dx, map_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
+    regs_dec<S::kRegsIssue>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      if (lane == 0) {
+        int j = 0;
+        bool ok = true;
+        for (int t = first; ok && t < p.tiles; t += step) {
+          int n0, g, m0;
+          tile(t, n0, g, m0);
+          const int w_row = g * p.N + n0;
+          const int x_row = m0 + (kPair ? rank * S::kRowsX : 0);  // a pair's MMA takes half of its tokens from each CTA
+          // Only rows that exist are loaded (the maps tm_xt, tm_wt have the boxes of the last rows): rows
+          // past the end cost a load more than rows do -- 4096 x 14 x 2048 took 15.4 us with boxes of 128
+          // rows of W, 6.4 us with 14.  What the missing rows of shared memory hold reaches only results
+          // that are not stored.
+          auto rows_of = [](int total, int at, int box) { return max(0, min(box, total - at)); };
+          const int w_rows = rows_of(p.N, n0, kTileN), x_rows = rows_of(p.M, x_row, S::kRowsX);
+          int rows = w_rows + x_rows;
+          if constexpr (kPair) rows += rows_of(p.N, n0 + kTileN, kTileN) + rows_of(p.M, x_row + S::kRowsX, S::kRowsX);  // the leader's count
+          const CUtensorMap* map_w = w_rows == kTileN ? &tm_w : &tm_wt;
+          const CUtensorMap* map_x = x_rows == S::kRowsX ? &tm_x : &tm_xt;
+          const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
+          for (int sl = slab0; sl < slab1; ++sl, ++j) {
+            const int st = j % S::kStages;
+            if (!mbar_wait(&empty[st], ((j / S::kStages) & 1) ^ 1, p.err, abort_flag)) {
+              ok = false;
+              break;
+            }
+            // codes past K and scale blocks past the end read as zeros or belong to columns that no MMA step
+            // covers, so every slab of a tile counts the same bytes
+            const int sf0 = sl * S::kAtoms;
+            const uint32_t dw = smem_u32(sW + st * S::kBytesW), dx = smem_u32(sX + st * S::kBytesX);
+            const uint32_t ds = smem_u32(sSf + st * S::kBytesSf);
+            mbar_arrive_expect_tx(&sf_full[st], S::kBytesSf);
+            tma_load_2d(ds, &tm_ws, &sf_full[st], 0, w_sf + sf0);
+            for (int rb = 0; rb < S::kRowBlocks; ++rb)
+              tma_load_2d(ds + 512 * S::kAtoms * (1 + rb), &tm_xs, &sf_full[st], 0, x_sf + rb * p.x_atoms + sf0);
+            if (leader) mbar_arrive_expect_tx(&full[st], rows * kSlabBytes);
+            if constexpr (kPair) {
+              const uint32_t bar = dsmem_map(&full[st], 0);
+              if (w_rows > 0) tma_load_2d_pair(dw, map_w, bar, sl * kSlabBytes, w_row);
+              if (x_rows > 0) tma_load_2d_pair(dx, map_x, bar, g * (p.K / 2) + sl * kSlabBytes, x_row);
+            } else {
+              tma_load_2d(dw, map_w, &full[st], sl * kSlabBytes, w_row);
+              tma_load_2d(dx, map_x, &full[st], g * (p.K / 2) + sl * kSlabBytes, x_row);
+            }
           }
         }
-      }
-      // the last loads issued must have landed before shared memory is reused or freed (of a pair: the
-      // leader waits for both CTAs' bytes, and the other CTA for the leader at the end)
-      volatile int never = 0;
-      for (int i = std::max(0, j - S::kStages); i < j; ++i) {
-        mbar_wait(&sf_full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
-        if (leader) mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
-      }
-    }
-    __syncwarp();
-   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    // The whole warp runs the loop and one lane is elected per slab: with a loop inside `lane == 0`
-    // the MMAs of a slab left the tensor pipe idle between them (698 against 512 cycles for a
-    // pair's slab, measured without loads).
-    if (leader) {
-      int j = 0, it = 0;
-      bool ok = true;
-      for (int t = first; ok && t < p.tiles; t += step, ++it) {
-        const int buf = it % S::kAcc;
-        if (!warp_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag)) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + kBN * buf;
-        for (int sl = slab0; sl < slab1; ++sl, ++j) {
-          const int st = j % S::kStages;
-          const uint32_t ph = (j / S::kStages) & 1;
-          if (!warp_wait(&sf_ready[st], ph, p.err, abort_flag) || !warp_wait(&full[st], ph, p.err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
-          const uint32_t sfw = tmem + S::kColSf + st * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
-          const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
-          auto mma = [&](int kk) {
-            const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
-            const uint64_t db = smem_desc(b0 + 32 * kk, 16, 1024, kSwizzle128B);
-            const uint32_t accumulate = (sl > slab0 || kk > 0) ? 1u : 0u;
-            constexpr int kRows = kTileN * S::kCtas;
-            if constexpr (kNv) {
-              const uint32_t a = sfw + 4 * kk, b = sfx + 4 * S::kRowBlocks * kk;
-              if constexpr (kPair)
-                mma_nvf4_pair(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
-              else
-                mma_nvf4(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
-            } else {
-              const uint32_t id = 2 * (kk & 1);  // the byte of the scale column of this K = 64 step
-              const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
-              if constexpr (kPair)
-                mma_mxf4_pair(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
-              else
-                mma_mxf4(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
-            }
-          };
-          if (elect_one()) {
-            if (n_mma == 4) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma(kk);
-            } else {
-              for (int kk = 0; kk < n_mma; ++kk) mma(kk);
-            }
-            commit(&empty[st]);
-            if (sl == slab1 - 1) commit(&acc_full[buf]);
-          }
-          __syncwarp();
+        // the last loads issued must have landed before shared memory is reused or freed (of a pair: the
+        // leader waits for both CTAs' bytes, and the other CTA for the leader at the end)
+        volatile int never = 0;
+        for (int i = std::max(0, j - S::kStages); i < j; ++i) {
+          mbar_wait(&sf_full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+          if (leader) mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
         }
-      }
-      if (elect_one()) {
-        if constexpr (kPair)
-          tc_commit_pair_local(fin);
-        else
-          tc_commit(fin);
       }
       __syncwarp();
-      volatile int never = 0;
-      mbar_wait(fin, 0, p.err, &never);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      // The whole warp runs the loop and one lane is elected per slab: with a loop inside `lane == 0`
+      // the MMAs of a slab left the tensor pipe idle between them (698 against 512 cycles for a
+      // pair's slab, measured without loads).
+      if (leader) {
+        int j = 0, it = 0;
+        bool ok = true;
+        for (int t = first; ok && t < p.tiles; t += step, ++it) {
+          const int buf = it % S::kAcc;
+          if (!warp_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + kBN * buf;
+          for (int sl = slab0; sl < slab1; ++sl, ++j) {
+            const int st = j % S::kStages;
+            const uint32_t ph = (j / S::kStages) & 1;
+            if (!warp_wait(&sf_ready[st], ph, p.err, abort_flag) || !warp_wait(&full[st], ph, p.err, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const int n_mma = min(4, (p.K - sl * kSlab + 63) / 64);
+            const uint32_t sfw = tmem + S::kColSf + st * S::kSfCols, sfx = sfw + 4 * S::kAtoms;
+            const uint32_t a0 = smem_u32(sW + st * S::kBytesW), b0 = smem_u32(sX + st * S::kBytesX);
+            auto mma = [&](int kk) {
+              const uint64_t da = smem_desc(a0 + 32 * kk, 16, 1024, kSwizzle128B);
+              const uint64_t db = smem_desc(b0 + 32 * kk, 16, 1024, kSwizzle128B);
+              const uint32_t accumulate = (sl > slab0 || kk > 0) ? 1u : 0u;
+              constexpr int kRows = kTileN * S::kCtas;
+              if constexpr (kNv) {
+                const uint32_t a = sfw + 4 * kk, b = sfx + 4 * S::kRowBlocks * kk;
+                if constexpr (kPair)
+                  mma_nvf4_pair(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
+                else
+                  mma_nvf4(acc, da, db, idesc_nvf4(kRows, kBN), accumulate, a, b);
+              } else {
+                const uint32_t id = 2 * (kk & 1);  // the byte of the scale column of this K = 64 step
+                const uint32_t a = (sfw + 4 * (kk >> 1)) | (id << 30), b = (sfx + 4 * S::kRowBlocks * (kk >> 1)) | (id << 30);
+                if constexpr (kPair)
+                  mma_mxf4_pair(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
+                else
+                  mma_mxf4(acc, da, db, idesc_mxf4(kRows, kBN, id, id), accumulate, a, b);
+              }
+            };
+            if (elect_one()) {
+              if (n_mma == 4) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma(kk);
+              } else {
+                for (int kk = 0; kk < n_mma; ++kk) mma(kk);
+              }
+              commit(&empty[st]);
+              if (sl == slab1 - 1) commit(&acc_full[buf]);
+            }
+            __syncwarp();
+          }
+        }
+        if (elect_one()) {
+          if constexpr (kPair)
+            tc_commit_pair_local(fin);
+          else
+            tc_commit(fin);
+        }
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(fin, 0, p.err, &never);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-   }
   } else if (warp < kOutWarp) {
     regs_dec<S::kRegsSf>();
     // ---------------------------------------------------------------- scales to TMEM (warps 4-7)
@@ -458,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           ok = false;
           break;
         }
+        tc_fence_after();  // the slot's last readers, of which the loads' barrier tells
         const uint4* src = reinterpret_cast<const uint4*>(sSf + st * S::kBytesSf) + lane;
         // a tile of 32 or 64 tokens takes its own columns of the row block's four
         constexpr int kUnits = S::kAtoms * (1 + S::kRowBlocks);

@@ -375,7 +375,8 @@ CSA_API csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d
 
 /*
  * Microscaled 4-bit matrices (the pages run the model's weights and the indexer in FP4; dev.to
- * "How DeepSeek-V4 Achieves ...").  A matrix [rows, cols], cols a multiple of 32, is
+ * "How DeepSeek-V4 Achieves ...").  A matrix [rows, cols], cols a multiple of 32
+ * and at most 2^30, is
  *   packed        uint8 [rows, cols/2]: E2M1 codes, element 2i in the low nibble of byte i;
  *   scales        uint8, one per block of a row's consecutive elements, in the layout below;
  *   tensor_scale  device float32, one value g > 0 (NVFP4), or NULL (MXFP4: g = 1).

@@ -53,7 +53,7 @@ def test_quantize_and_dequantize_refusals(B):
         assert f(fmt=2) == INVALID and f(rows=-1) == INVALID and f(cols=0) == INVALID and f(cols=48) == INVALID
         assert f(ld=32) == INVALID and f(dt=2) == INVALID
         assert f(ld=68) == ALIGNMENT and f(ld=66, dt=F32) == ALIGNMENT
-        assert f(rows=0) == 0
+        assert f(rows=0) == 0 and f(cols=(1 << 30) + 32, ld=1 << 31) == UNSUPPORTED
     assert q(x=None) == INVALID and q(x=P(24)) == ALIGNMENT and d(y=None) == INVALID and d(y=P(24)) == ALIGNMENT
     for kw in ("out", "m"):
         f = q if kw == "out" else d
@@ -67,6 +67,8 @@ def test_quantize_and_dequantize_refusals(B):
     assert L.csa_fp4_pack_scales(MX, P(3), 4, 64, P(17), None) == ALIGNMENT
     assert L.csa_fp4_pack_scales(MX, P(3), 4, 40, P(16), None) == INVALID
     assert L.csa_fp4_pack_scales(MX, None, 0, 64, None, None) == 0
+    assert L.csa_fp4_pack_scales(MX, P(3), 4, (1 << 30) + 32, P(16), None) == UNSUPPORTED
+    assert L.csa_fp4_scale_bytes(MX, 4, (1 << 30) + 32) == 0
 
 
 def test_linear_refusals(B):
