@@ -503,8 +503,9 @@ csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d_model, 
 }
 
 // ------------------------------------------------------------------ microscaled 4-bit matrices
-// columns are counted in int with room for a warp's overshoot
-static constexpr int64_t kFp4MaxCols = int64_t(1) << 30;
+// columns, and a product's rows, are counted in int with room for a warp's or a tile's overshoot;
+// the rows of a matrix in int64
+static constexpr int64_t kFp4MaxCols = int64_t(1) << 30, kFp4MaxRows = int64_t(1) << 40;
 static bool fp4_format_ok(csa_fp4_format f) { return f == CSA_MXFP4 || f == CSA_NVFP4; }
 
 // A matrix argument of rows x cols: pointers present and aligned, a tensor scale with NVFP4 only.
@@ -517,7 +518,7 @@ static csa_status fp4_mat_status(csa_fp4_format f, const csa_fp4_mat* m) {
 }
 
 size_t csa_fp4_scale_bytes(csa_fp4_format fmt, int64_t rows, int cols) {
-  if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols > kFp4MaxCols) return 0;
+  if (!fp4_format_ok(fmt) || rows < 0 || rows > kFp4MaxRows || cols < 1 || cols > kFp4MaxCols) return 0;
   return fp4_scale_bytes(fmt == CSA_NVFP4, rows, cols);
 }
 
@@ -525,7 +526,7 @@ csa_status csa_fp4_quantize(csa_fp4_format fmt, const void* x, csa_dtype dtype, 
                             const csa_fp4_mat* out, cudaStream_t stream) {
   if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0 || ld < cols) return CSA_ERR_INVALID_ARG;
   if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
-  if (cols > kFp4MaxCols) return CSA_ERR_UNSUPPORTED;
+  if (cols > kFp4MaxCols || rows > kFp4MaxRows) return CSA_ERR_UNSUPPORTED;
   if (rows == 0) return CSA_OK;
   if (x == nullptr) return CSA_ERR_INVALID_ARG;
   const csa_status st = fp4_mat_status(fmt, out);
@@ -539,7 +540,7 @@ csa_status csa_fp4_dequantize(csa_fp4_format fmt, const csa_fp4_mat* m, int64_t 
                               void* out, int64_t ld, cudaStream_t stream) {
   if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0 || ld < cols) return CSA_ERR_INVALID_ARG;
   if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_ERR_INVALID_ARG;
-  if (cols > kFp4MaxCols) return CSA_ERR_UNSUPPORTED;
+  if (cols > kFp4MaxCols || rows > kFp4MaxRows) return CSA_ERR_UNSUPPORTED;
   if (rows == 0) return CSA_OK;
   if (out == nullptr) return CSA_ERR_INVALID_ARG;
   const csa_status st = fp4_mat_status(fmt, m);
@@ -552,7 +553,7 @@ csa_status csa_fp4_dequantize(csa_fp4_format fmt, const csa_fp4_mat* m, int64_t 
 csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales, int64_t rows, int cols, uint8_t* out,
                                cudaStream_t stream) {
   if (!fp4_format_ok(fmt) || rows < 0 || cols < 1 || cols % 32 != 0) return CSA_ERR_INVALID_ARG;
-  if (cols > kFp4MaxCols) return CSA_ERR_UNSUPPORTED;
+  if (cols > kFp4MaxCols || rows > kFp4MaxRows) return CSA_ERR_UNSUPPORTED;
   if (rows == 0) return CSA_OK;
   if (scales == nullptr || out == nullptr) return CSA_ERR_INVALID_ARG;
   if (!aligned16(out)) return CSA_ERR_ALIGNMENT;
@@ -564,7 +565,7 @@ csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales, int64_
 static csa_status fp4_product_status(int64_t M, int64_t N, int64_t K, int64_t G) {
   if (M < 0 || N < 1 || K < 1 || G < 1) return CSA_ERR_INVALID_ARG;
   if (K % 32 != 0 || (G > 1 && (K % 128 != 0 || N % 128 != 0))) return CSA_ERR_UNSUPPORTED;
-  if (G * K > kFp4MaxCols || G * N > kFp4MaxCols) return CSA_ERR_UNSUPPORTED;
+  if (M > kFp4MaxCols || G * K > kFp4MaxCols || G * N > kFp4MaxCols) return CSA_ERR_UNSUPPORTED;
   return CSA_OK;
 }
 
@@ -599,7 +600,7 @@ csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const 
 size_t csa_grouped_out_proj_fp4_workspace(csa_fp4_format fmt, int T, int H, int D, int G, int R) {
   if (!fp4_format_ok(fmt) || T < 0 || H < 1 || D < 1 || G < 1 || R < 1) return 0;
   const int64_t HD = static_cast<int64_t>(H) * D, GR = static_cast<int64_t>(G) * R;
-  if (HD > kFp4MaxCols || GR > kFp4MaxCols) return 0;
+  if (T > kFp4MaxCols || HD > kFp4MaxCols || GR > kFp4MaxCols) return 0;
   return fp4_proj_workspace_bytes(fmt == CSA_NVFP4, T, HD, GR);
 }
 

@@ -376,7 +376,7 @@ CSA_API csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d
 /*
  * Microscaled 4-bit matrices (the pages run the model's weights and the indexer in FP4; dev.to
  * "How DeepSeek-V4 Achieves ...").  A matrix [rows, cols], cols a multiple of 32
- * and at most 2^30, is
+ * and at most 2^30 (rows at most 2^40), is
  *   packed        uint8 [rows, cols/2]: E2M1 codes, element 2i in the low nibble of byte i;
  *   scales        uint8, one per block of a row's consecutive elements, in the layout below;
  *   tensor_scale  device float32, one value g > 0 (NVFP4), or NULL (MXFP4: g = 1).
@@ -427,7 +427,8 @@ CSA_API csa_status csa_fp4_pack_scales(csa_fp4_format fmt, const uint8_t* scales
  * rounding to y_dtype.  The result never depends on timing; it may differ with M in the last
  * bits, since K is split over CTAs when there are few tiles (never with csa_set_batch_invariant
  * on: a row's result is then the same whatever the other rows).
- * Supported: K a multiple of 32; with G > 1, K and N multiples of 128.  No workspace.
+ * Supported: K a multiple of 32; with G > 1, K and N multiples of 128; M, G K and G N at most 2^30.
+ * No workspace.
  */
 CSA_API csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x,
                                   const csa_fp4_mat* w, csa_dtype y_dtype, void* y, int64_t ldy, cudaStream_t stream);
@@ -438,7 +439,7 @@ CSA_API csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G
  * matrix, z rounded to bf16 and encoded with z_scale, then multiplied by Bm; y bf16 [T, d_model].
  * o_scale, z_scale: device float32 tensor scales (NVFP4; calibrated by the caller), NULL for MXFP4.
  * workspace: csa_grouped_out_proj_fp4_workspace bytes (0 for invalid arguments).
- * Supported: (H/G) D and R multiples of 128.
+ * Supported: (H/G) D and R multiples of 128; T, H D and G R at most 2^30.
  */
 CSA_API size_t csa_grouped_out_proj_fp4_workspace(csa_fp4_format fmt, int T, int H, int D, int G, int R);
 CSA_API csa_status csa_grouped_out_proj_fp4(csa_fp4_format fmt, int T, int H, int D, int G, int R, int d_model,

@@ -177,3 +177,17 @@ def test_reference_nvfp4_error_bound():
     T = np.repeat(R.E4M3[sb] * float(g), 16, 1)
     # the scale rounds down by at most 2^-4, so the largest code clips at most 6 (1 + 2^-4) - 6 = 0.375 T
     assert (np.abs(v - x) <= T * (1.0 + 1e-6)).all()
+
+
+def test_refuses_more_rows_than_it_counts(B):
+    L, P, BIG = B.lib(), ctypes.c_void_p, (1 << 30) + 1
+    m = mat(B)
+    assert L.csa_fp4_linear(MX, BIG, 256, 256, 1, m, m, BF16, P(16), 256, None) == UNSUPPORTED
+    assert L.csa_grouped_out_proj_fp4_workspace(MX, BIG, 4, 128, 2, 128) == 0
+    assert L.csa_grouped_out_proj_fp4(MX, BIG, 4, 128, 2, 128, 64, P(16), None, m, None, m, P(16), P(16), 1 << 62,
+                                      None) == UNSUPPORTED
+    rows = (1 << 40) + 1
+    assert L.csa_fp4_scale_bytes(MX, rows, 64) == 0
+    assert L.csa_fp4_quantize(MX, P(16), BF16, rows, 64, 64, m, None) == UNSUPPORTED
+    assert L.csa_fp4_dequantize(MX, m, rows, 64, BF16, P(16), 64, None) == UNSUPPORTED
+    assert L.csa_fp4_pack_scales(MX, P(16), rows, 64, P(16), None) == UNSUPPORTED
