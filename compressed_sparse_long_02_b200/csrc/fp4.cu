@@ -99,7 +99,7 @@ struct RowTask {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       float v[8];
-      raw[u].values(v);
+      raw[u].template values<kNv>(v);
       word[u] = kNv ? nv_codes8(v, T, am) : e2m1x8_rn(v, T);
     }
     if (in) {
@@ -255,8 +255,8 @@ Fp4Shape fp4_shape(bool nv, int64_t rows, int cols, int64_t ld, int chunk) {
 }
 
 // One warp per task up to `per_sm` CTAs per SM, a loop beyond.  The encoder takes eight (four,
-// NVFP4 three, run at once; NVFP4's set-up makes more CTAs dearer: 8192 x 32768 bf16 130 us, 136 with 64),
-// the decoder as many as there are tasks up to 64 (the same size: 119 us with 8, 114 with 16, 105 with 64).
+// NVFP4 three, run at once; NVFP4's set-up makes more CTAs dearer: 8192 x 32768 bf16 5% slower with 64),
+// the decoder as many as there are tasks up to 64 (that size: 119 us with 8, 114 with 16, 105 with 64).
 unsigned fp4_grid(int64_t n_tasks, int per_sm) {
   const int64_t blocks = (n_tasks + kFp4Threads / 32 - 1) / (kFp4Threads / 32);
   return static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms()) * per_sm));

@@ -85,12 +85,45 @@ __device__ __forceinline__ void nv_quotients(float (&v)[kN], float T, float amax
   for (int i = 0; i < kN; ++i) v[i] = y[i];
 }
 
-// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T).
-__device__ __forceinline__ uint32_t nv_codes8(const float (&v)[8], float T, float amax) {
+// pairs of float32 in one 64-bit register: two roundings an instruction
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+
+// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T), zeros if T is zero.  Takes
+// the values negated (nx = -x), as the packed residuals q T - x want them; the steps are
+// div_given_rcp's, with plain division where nv_quotients takes it.
+__device__ __forceinline__ uint32_t nv_codes8(const float (&nx)[8], float T, float amax) {
+  const float r = __frcp_rn(T);
+  const uint64_t T2 = f32x2(T, T), nr2 = f32x2(-r, -r);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = v[i];
-  nv_quotients(y, T, amax);
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t n2 = f32x2(nx[i], nx[i + 1]);
+    uint64_t q = mul_f32x2(n2, nr2);
+    q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
+    q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y[i]), "=f"(y[i + 1]) : "l"(q));
+  }
+  if (!(div_range(T) && amax <= 8.f * T)) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 q = div4(nx[i], nx[i + 1], nx[i + 2], nx[i + 3], -T);
+      y[i] = q.x, y[i + 1] = q.y, y[i + 2] = q.z, y[i + 3] = q.w;
+    }
+  }
   return e2m1x8_rn(y, 1.f);
 }
 
@@ -129,6 +162,13 @@ __device__ __forceinline__ float bf16x8_amax(const uint4& u) {
   return fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), 0.f);
 }
 
+// a pair of bf16 as floats, or as floats negated (a shift and add, as one instruction, flips the sign)
+template <bool kNeg>
+__device__ __forceinline__ void bf16x2_floats(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float((w << 16) + (kNeg ? 0x80000000u : 0u));
+  hi = __uint_as_float((w & 0xFFFF0000u) ^ (kNeg ? 0x80000000u : 0u));
+}
+
 // eight values as they lie in memory (16 bytes of bf16, 32 of float32), and as floats
 template <bool kBf16>
 struct Raw8;
@@ -140,13 +180,11 @@ struct Raw8<true> {
   }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ float amax() const { return bf16x8_amax(u); }
+  template <bool kNeg>  // (negated: as nv_codes8 takes them)
   __device__ __forceinline__ void values(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) bf16x2_floats<kNeg>(w[i], v[2 * i], v[2 * i + 1]);
   }
 };
 template <>
@@ -163,9 +201,14 @@ struct Raw8<false> {
     const float m1 = fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w)));
     return fmaxf(fmaxf(m0, m1), 0.f);
   }
+  template <bool kNeg>
   __device__ __forceinline__ void values(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    if constexpr (kNeg) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = -v[i];
+    }
   }
 };
 

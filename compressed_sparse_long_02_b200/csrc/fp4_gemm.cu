@@ -170,10 +170,7 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
   for (int q = 0; q < 4; ++q) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[4 * q + i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[4 * q + i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) bf16x2_floats<kNv>(w[4 * q + i], v[2 * i], v[2 * i + 1]);
     codes[q] = kNv ? nv_codes8(v, inv[q / 2], top[q / 2]) : e2m1x8_rn(v, inv[q / 2]);
   }
   const int lane = threadIdx.x & 31;
