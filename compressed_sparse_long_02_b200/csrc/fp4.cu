@@ -15,7 +15,7 @@
 //
 // All three kernels are bound by HBM: 2 or 4 bytes read and 17/32 or 9/16 written per element.
 // 8192 x 32768 bf16 on one B200: MXFP4 encoding 102 us (6.7 TB/s, the copy rate) and decoding 105;
-// NVFP4 123 us (5.6 TB/s: its quotients keep the issue slots 70% busy at 24 warps an SM) and 106.
+// NVFP4 123 us (5.6 TB/s: about 200 instructions for 16 values of a lane, MXFP4 160) and 106.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -80,8 +80,9 @@ struct RowTask {
         raw[u].zero();
     }
   }
-  // stores the codes (where `in`) and returns the atom's four scale bytes, in each of its lanes
-  __device__ __forceinline__ uint32_t encode(const NvScale& nv, uint8_t* packed, int64_t at, bool in) const {
+  // stores the codes (where `in`) and returns the atom's four scale bytes, in each of its lanes;
+  // `plain` is set where the codes need plain division: see encode_plain
+  __device__ __forceinline__ uint32_t encode(const NvScale& nv, uint8_t* packed, int64_t at, bool in, bool& plain) const {
     const int lane = threadIdx.x & 31;
     float am = raw[0].amax();
 #pragma unroll
@@ -93,16 +94,18 @@ struct RowTask {
     if constexpr (kNv) {
       byte = nv.byte(am);
       T = e4m3_value(byte) * nv.g;
+      plain = T != 0.f && nv_plain(T, am);
     } else {
       const int E = mx_block_exponent(am);
       T = mx_pow2_neg(E);
       byte = static_cast<uint32_t>(E + 127);
     }
+    const float r = kNv ? __frcp_rn(T) : 0.f;
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       float v[8];
       raw[u].template values<kNv>(v);
-      word[u] = kNv ? nv_codes8(v, T, am) : e2m1x8_rn(v, T);
+      word[u] = kNv ? (T == 0.f ? 0u : nv_codes8_common(v, T, r)) : e2m1x8_rn(v, T);
     }
     if (in) {
       if constexpr (kUnits == 2)
@@ -117,8 +120,24 @@ struct RowTask {
   }
 };
 
+// The codes of a lane's share of a row by plain division, over what encode() stored (out of line, from
+// memory again: extreme scales only, and the common path keeps no values for it).
+template <bool kBf16>
+static __device__ __noinline__ void encode_plain(const void* x, int64_t at, float T, uint8_t* packed, int64_t at_codes) {
+#pragma unroll 1
+  for (int u = 0; u < kEncodePer<kBf16>; u += 8) {
+    Raw8<kBf16> raw;
+    raw.load(x, at + u);
+    float v[8];
+    raw.template values<true>(v);
+    *reinterpret_cast<uint32_t*>(packed + (at_codes + u) / 2) = nv_codes8_plain(v, T);
+  }
+}
+
+// (four CTAs an SM asked for where it pays: NVFP4 from float32, 8192 x 32768, 198 -> 186 us; the other
+// three reach four by themselves, 0 being no request)
 template <bool kBf16, bool kNv>
-__global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* __restrict__ x, Fp4Shape p,
+__global__ void __launch_bounds__(kFp4Threads, kNv && !kBf16 ? 4 : 0) fp4_quantize_kernel(const void* __restrict__ x, Fp4Shape p,
                                                                    const float* __restrict__ tensor_scale,
                                                                    uint8_t* __restrict__ packed,
                                                                    uint8_t* __restrict__ scales) {
@@ -134,12 +153,13 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
     const int col = t.chunk * kEncodeChunk<kBf16> + lane * RT::kPer;
     const bool in = col < p.cols;  // cols is a multiple of 32: a lane's columns are all in or all out
     uint32_t w[4] = {0, 0, 0, 0};
+    bool plain[4] = {false, false, false, false};
     if (row0 + 96 < p.rows) {
       RT rt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) rt[i].load(x, (row0 + 32 * i) * p.ld + col, in);  // every load first
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(nv, packed, (row0 + 32 * i) * p.cols + col, in);
+      for (int i = 0; i < 4; ++i) w[i] = rt[i].encode(nv, packed, (row0 + 32 * i) * p.cols + col, in, plain[i]);
     } else {  // the last row block: one row at a time, so that rows that only pad it cost nothing
       RT rt;
       rt.load(x, row0 * p.ld + col, in && row0 < p.rows);
@@ -147,9 +167,11 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
       for (int64_t row = row0; row < p.rows; row += 32) {
         RT next;
         next.load(x, (row + 32) * p.ld + col, in && row + 32 < p.rows);
-        const uint32_t v = rt.encode(nv, packed, row * p.cols + col, in);
+        bool pl = false;
+        const uint32_t v = rt.encode(nv, packed, row * p.cols + col, in, pl);
         rt = next;
         const int i = static_cast<int>((row - row0) / 32);
+        plain[0] |= i == 0 && pl, plain[1] |= i == 1 && pl, plain[2] |= i == 2 && pl;
         w[0] = i == 0 ? v : w[0];
         w[1] = i == 1 ? v : w[1];
         w[2] = i == 2 ? v : w[2];
@@ -158,6 +180,14 @@ __global__ void __launch_bounds__(kFp4Threads) fp4_quantize_kernel(const void* _
     const int atom = (t.chunk * 32 + lane) / RT::kAtomLanes;
     if (lane % RT::kAtomLanes == 0 && atom < p.n_atoms)
       *reinterpret_cast<uint4*>(scales + fp4_atom_offset(t.row >> 5, atom, p.n_atoms) + r32 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (kNv) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + 32 * i;
+        const uint32_t byte = (w[i] >> (8 * ((lane / RT::kBlkLanes) & 3))) & 0xFFu;
+        if (plain[i] && in) encode_plain<kBf16>(x, row * p.ld + col, e4m3_value(byte) * nv.g, packed, row * p.cols + col);
+      }
+    }
   }
 }
 
@@ -256,8 +286,8 @@ Fp4Shape fp4_shape(bool nv, int64_t rows, int cols, int64_t ld, int chunk) {
   return p;
 }
 
-// One warp per task up to `per_sm` CTAs per SM, a loop beyond.  The encoder takes eight (four,
-// NVFP4 three, run at once; NVFP4's set-up makes more CTAs dearer: 8192 x 32768 bf16 5% slower with 64),
+// One warp per task up to `per_sm` CTAs per SM, a loop beyond.  The encoder takes eight (four
+// run at once; NVFP4's set-up makes more CTAs dearer: 8192 x 32768 bf16 5% slower with 64),
 // the decoder as many as there are tasks up to 64 (that size: 119 us with 8, 114 with 16, 105 with 64).
 unsigned fp4_grid(int64_t n_tasks, int per_sm) {
   const int64_t blocks = (n_tasks + kFp4Threads / 32 - 1) / (kFp4Threads / 32);

@@ -49,6 +49,9 @@ static __device__ __noinline__ float4 div4(float a, float b, float c, float d, f
 // The range of divisors that div_given_rcp takes.
 __device__ __forceinline__ bool div_range(float T) { return T >= 0x1p-90f && T <= 0x1p100f; }
 
+// Whether a block's quotients take plain division: a scale cut at 448, or a T out of range.
+__device__ __forceinline__ bool nv_plain(float T, float amax) { return !(div_range(T) && amax <= 8.f * T); }
+
 // NVFP4's encoder constants of a tensor: its scale g, and 6 g with the reciprocal.
 struct NvScale {
   float g, six_g, rcp;
@@ -74,7 +77,7 @@ __device__ __forceinline__ void nv_quotients(float (&v)[kN], float T, float amax
   float y[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) y[i] = div_given_rcp(v[i], T, r);
-  if (!(div_range(T) && amax <= 8.f * T)) {
+  if (nv_plain(T, amax)) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
       const float4 q = div4(v[i], v[i + 1], v[i + 2], v[i + 3], T);
@@ -102,11 +105,10 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   return v;
 }
 
-// Codes of eight values of a block under its NVFP4 scale T: e2m1(x / T), zeros if T is zero.  Takes
-// the values negated (nx = -x), as the packed residuals q T - x want them; the steps are
-// div_given_rcp's, with plain division where nv_quotients takes it.
-__device__ __forceinline__ uint32_t nv_codes8(const float (&nx)[8], float T, float amax) {
-  const float r = __frcp_rn(T);
+// Codes of eight values of a block under its NVFP4 scale T, e2m1(x / T), where !nv_plain; r is 1 / T
+// correctly rounded.  Takes the values negated (nx = -x), as the packed residuals q T - x want them;
+// the steps are div_given_rcp's.
+__device__ __forceinline__ uint32_t nv_codes8_common(const float (&nx)[8], float T, float r) {
   const uint64_t T2 = f32x2(T, T), nr2 = f32x2(-r, -r);
   float y[8];
 #pragma unroll
@@ -117,14 +119,17 @@ __device__ __forceinline__ uint32_t nv_codes8(const float (&nx)[8], float T, flo
     q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
     asm("mov.b64 {%0, %1}, %2;" : "=f"(y[i]), "=f"(y[i + 1]) : "l"(q));
   }
-  if (!(div_range(T) && amax <= 8.f * T)) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      const float4 q = div4(nx[i], nx[i + 1], nx[i + 2], nx[i + 3], -T);
-      y[i] = q.x, y[i + 1] = q.y, y[i + 2] = q.z, y[i + 3] = q.w;
-    }
-  }
   return e2m1x8_rn(y, 1.f);
+}
+// the same by plain division, zeros for T = 0
+__device__ __forceinline__ uint32_t nv_codes8_plain(const float (&nx)[8], float T) {
+  const float4 a = div4(nx[0], nx[1], nx[2], nx[3], -T), b = div4(nx[4], nx[5], nx[6], nx[7], -T);
+  const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return e2m1x8_rn(y, 1.f);
+}
+__device__ __forceinline__ uint32_t nv_codes8(const float (&nx)[8], float T, float amax) {
+  const uint32_t w = nv_codes8_common(nx, T, __frcp_rn(T));
+  return nv_plain(T, amax) ? nv_codes8_plain(nx, T) : w;
 }
 
 // 2^(byte - 127); byte 255 is NaN, byte 0 the subnormal 2^-127
