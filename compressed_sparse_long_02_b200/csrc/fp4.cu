@@ -15,7 +15,7 @@
 //
 // All three kernels are bound by HBM: 2 or 4 bytes read and 17/32 or 9/16 written per element.
 // 8192 x 32768 bf16 on one B200: MXFP4 encoding 102 us (6.7 TB/s, the copy rate) and decoding 105;
-// NVFP4 123 us (5.6 TB/s: about 200 instructions for 16 values of a lane, MXFP4 160) and 106.
+// NVFP4 113 us (6.1 TB/s: about 180 instructions for 16 values of a lane, MXFP4 160) and 106.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -94,7 +94,7 @@ struct RowTask {
     if constexpr (kNv) {
       byte = nv.byte(am);
       T = e4m3_value(byte) * nv.g;
-      plain = T != 0.f && nv_plain(T, am);
+      plain = T != 0.f && nv_plain<kBf16>(T, am);
     } else {
       const int E = mx_block_exponent(am);
       T = mx_pow2_neg(E);
@@ -105,7 +105,7 @@ struct RowTask {
     for (int u = 0; u < kUnits; ++u) {
       float v[8];
       raw[u].template values<kNv>(v);
-      word[u] = kNv ? (T == 0.f ? 0u : nv_codes8_common(v, T, r)) : e2m1x8_rn(v, T);
+      word[u] = kNv ? (T == 0.f ? 0u : nv_codes8_common<kBf16>(v, T, r)) : e2m1x8_rn(v, T);
     }
     if (in) {
       if constexpr (kUnits == 2)

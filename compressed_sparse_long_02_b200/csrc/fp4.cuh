@@ -49,8 +49,12 @@ static __device__ __noinline__ float4 div4(float a, float b, float c, float d, f
 // The range of divisors that div_given_rcp takes.
 __device__ __forceinline__ bool div_range(float T) { return T >= 0x1p-90f && T <= 0x1p100f; }
 
-// Whether a block's quotients take plain division: a scale cut at 448, or a T out of range.
-__device__ __forceinline__ bool nv_plain(float T, float amax) { return !(div_range(T) && amax <= 8.f * T); }
+// Whether a block's quotients take plain division: a scale cut at 448, a T out of range, or (bf16 values)
+// one whose significand is all ones (see nv_codes8_common).
+template <bool kBf16>
+__device__ __forceinline__ bool nv_plain(float T, float amax) {
+  return !(div_range(T) && amax <= 8.f * T) || (kBf16 && (__float_as_uint(T) & 0x7FFFFFu) == 0x7FFFFFu);
+}
 
 // NVFP4's encoder constants of a tensor: its scale g, and 6 g with the reciprocal.
 struct NvScale {
@@ -77,7 +81,7 @@ __device__ __forceinline__ void nv_quotients(float (&v)[kN], float T, float amax
   float y[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) y[i] = div_given_rcp(v[i], T, r);
-  if (nv_plain(T, amax)) {
+  if (nv_plain<false>(T, amax)) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
       const float4 q = div4(v[i], v[i + 1], v[i + 2], v[i + 3], T);
@@ -107,7 +111,15 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
 
 // Codes of eight values of a block under its NVFP4 scale T, e2m1(x / T), where !nv_plain; r is 1 / T
 // correctly rounded.  Takes the values negated (nx = -x), as the packed residuals q T - x want them;
-// the steps are div_given_rcp's.
+// the steps are div_given_rcp's.  For x of 8 bits (bf16) one step gives the same codes: it leaves
+// q1 = fl(x / T (1 + e)), |e| < 2^-46, which can fall on another side of a code's border t (an odd
+// multiple of 1/4 up to 5, t = J 2^n with J = 1, 3, 5, 7) than fl(x / T) only if x / T is that close to
+// the middle M of t and a neighbour.  As integers, M = J 2^s +- 1 of 25 bits (s >= 22), T of 24, x of 8
+// at the same scale: M T would be within 8 of a multiple of 2^41.  Modulo 2^22 that makes T = c 2^22 + d
+// with |d| <= 8 and c = 2, 3 or 4; what remains is J d 2^s +- c 2^22 +- d within 8 of 0, so
+// J d 2^(s - 22) = -+ c, which has one solution: J = 1, s = 24, c = 4, d = -1, T = 2^24 - 1 (a run over
+// all T and M finds no other).
+template <bool kBf16>
 __device__ __forceinline__ uint32_t nv_codes8_common(const float (&nx)[8], float T, float r) {
   const uint64_t T2 = f32x2(T, T), nr2 = f32x2(-r, -r);
   float y[8];
@@ -115,7 +127,7 @@ __device__ __forceinline__ uint32_t nv_codes8_common(const float (&nx)[8], float
   for (int i = 0; i < 8; i += 2) {
     const uint64_t n2 = f32x2(nx[i], nx[i + 1]);
     uint64_t q = mul_f32x2(n2, nr2);
-    q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
+    if constexpr (!kBf16) q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
     q = fma_f32x2(fma_f32x2(q, T2, n2), nr2, q);
     asm("mov.b64 {%0, %1}, %2;" : "=f"(y[i]), "=f"(y[i + 1]) : "l"(q));
   }
@@ -126,10 +138,6 @@ __device__ __forceinline__ uint32_t nv_codes8_plain(const float (&nx)[8], float 
   const float4 a = div4(nx[0], nx[1], nx[2], nx[3], -T), b = div4(nx[4], nx[5], nx[6], nx[7], -T);
   const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   return e2m1x8_rn(y, 1.f);
-}
-__device__ __forceinline__ uint32_t nv_codes8(const float (&nx)[8], float T, float amax) {
-  const uint32_t w = nv_codes8_common(nx, T, __frcp_rn(T));
-  return nv_plain(T, amax) ? nv_codes8_plain(nx, T) : w;
 }
 
 // 2^(byte - 127); byte 255 is NaN, byte 0 the subnormal 2^-127

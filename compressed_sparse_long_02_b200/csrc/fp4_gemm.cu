@@ -138,15 +138,35 @@ __device__ __forceinline__ uint32_t part_at(int tok, int chunk) {  // chunk: 8 f
   return static_cast<uint32_t>((chunk >> 3) * kPart * 128 + tok * 128 + (((chunk & 7) ^ (tok & 7)) << 4));
 }
 
-// Encodes 32 consecutive features (feat, a multiple of 32) of one bf16 token; four neighbouring
-// lanes hold the four quarters of 128 features of one token and join their scale bytes.
+// The codes of 16 of those features by plain division, from the part's buffer again (out of line:
+// extreme scales only).
+static __device__ __noinline__ uint2 part_codes_plain(const uint8_t* buf, int tok, int chunk, float T) {
+  uint32_t codes[2];
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    const uint4 x = *reinterpret_cast<const uint4*>(buf + part_at(tok, chunk + q));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bf16x2_floats<true>(w[i], v[2 * i], v[2 * i + 1]);
+    codes[q] = nv_codes8_plain(v, T);
+  }
+  return make_uint2(codes[0], codes[1]);
+}
+
+// Encodes 32 consecutive features (feat, a multiple of 32) of one bf16 token of a part's buffer; four
+// neighbouring lanes hold the four quarters (b) of 128 features of one token and join their scale bytes.
 template <bool kNv>
-__device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, int feat, int n_feat, int n_atoms,
+__device__ __forceinline__ void encode_32(const uint8_t* buf, int tok, int b, bool in, int m, int feat, int n_feat, int n_atoms,
                                           const LinearParams& p, const NvScale& nv) {
+  uint4 x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(buf + part_at(tok, 4 * b + j));
   const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
   uint32_t codes[4], bytes = 0;
-  float inv[2], top[2];
+  float inv[2], top[2], rcp[2];
+  bool plain[2] = {false, false};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // halves of 16: a block each (NVFP4) or together (MXFP4)
     uint32_t am = 0;
@@ -160,6 +180,8 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
       const uint32_t byte = nv.byte(top[h]);
       bytes |= byte << (8 * h);
       inv[h] = e4m3_value(byte) * nv.g;  // T
+      rcp[h] = __frcp_rn(inv[h]);
+      plain[h] = inv[h] != 0.f && nv_plain<true>(inv[h], top[h]);
     }
   } else {
     const int E = mx_block_exponent(fmaxf(top[0], top[1]));
@@ -171,7 +193,7 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
     float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) bf16x2_floats<kNv>(w[4 * q + i], v[2 * i], v[2 * i + 1]);
-    codes[q] = kNv ? nv_codes8(v, inv[q / 2], top[q / 2]) : e2m1x8_rn(v, inv[q / 2]);
+    codes[q] = kNv ? (inv[q / 2] == 0.f ? 0u : nv_codes8_common<true>(v, inv[q / 2], rcp[q / 2])) : e2m1x8_rn(v, inv[q / 2]);
   }
   const int lane = threadIdx.x & 31;
   if constexpr (kNv) {  // two bytes per lane: lanes 0, 1 hold one atom's four scales, lanes 2, 3 the next's
@@ -181,6 +203,15 @@ __device__ __forceinline__ void encode_32(const uint4 (&x)[4], bool in, int m, i
     bytes <<= 8 * (lane & 3);
     bytes |= __shfl_xor_sync(0xffffffffu, bytes, 1);
     bytes |= __shfl_xor_sync(0xffffffffu, bytes, 2);
+  }
+  if constexpr (kNv) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (in && plain[h]) {
+        const uint2 c = part_codes_plain(buf, tok, 4 * b + 2 * h, inv[h]);
+        codes[2 * h] = c.x, codes[2 * h + 1] = c.y;
+      }
+    }
   }
   if (in) {
     *reinterpret_cast<uint4*>(p.z_packed + (static_cast<int64_t>(m) * n_feat + feat) / 2) =
@@ -626,10 +657,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           if constexpr (kOut == kOutFp4) {
             named_bar_sync(1 + half, 128);
             const int tok = id / 4, b = id % 4;
-            uint4 x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(buf_z + part_at(tok, 4 * b + j));
-            encode_32<kNv>(x, tok < left && n0 < p.N, m + tok, g * p.N + n0 + 32 * b, p.G * p.N, p.z_atoms, p, nvz);
+            encode_32<kNv>(buf_z, tok, b, tok < left && n0 < p.N, m + tok, g * p.N + n0 + 32 * b, p.G * p.N, p.z_atoms, p, nvz);
           } else if (p.tma_y) {
             fence_proxy_async_smem();
             if (id == 0) bulk_wait_read();  // the other buffer's store has read it

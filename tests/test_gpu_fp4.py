@@ -123,6 +123,41 @@ def test_encode_borders_and_special_values(B, cuda, fmt):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nvfp4_quotients_next_to_every_border(B, cuda, dtype):
+    """x = t T and its neighbours in x's type for every border t and block scales T of many significands,
+    all ones and its neighbours among them: a code is e2m1(fl(x / T)), to the bit."""
+    rng = np.random.default_rng(5)
+    sig = np.concatenate([[2 ** 24 - 1, 2 ** 24 - 2, 2 ** 24 - 3, 2 ** 23, 2 ** 23 + 1, 2 ** 23 + 2, 11184810, 11184811,
+                           5 * 2 ** 21 + 1, 7 * 2 ** 21 - 1, 2 ** 22 * 3 - 1, 2 ** 22 * 3 + 1],
+                          rng.integers(2 ** 23, 2 ** 24, 40)]).astype(np.float64)
+    step = 1 if dtype is torch.float32 else 2 ** 16  # between neighbours, in float32 bits
+    for s, e in zip(sig, rng.integers(-40, 20, len(sig))):
+        g = np.float32(s * 2.0 ** int(e))
+        rows = []
+        for sc in (1.0, 1.125, 13.0, 448.0):  # the block's E4M3 scale
+            T = np.float32(sc) * g
+            top = np.float32(6.0) * T
+            t = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], np.float32) * T
+            bits = t.view(np.int32) // step * step
+            x = np.concatenate([(bits + step * d).view(np.float32) for d in (-2, -1, 0, 1, 2)])
+            x = np.concatenate([x, -x, [0.0, -0.0]]).astype(np.float32)
+            for k in range(0, len(x), 15):
+                c = x[k:k + 15]
+                topb = (top.view(np.int32) // step * step).view(np.float32)
+                rows.append(np.concatenate([[topb], c, np.zeros(15 - len(c), np.float32)]))
+        if len(rows) % 2:
+            rows.append(rows[0])
+        x = np.stack(rows).astype(np.float32).reshape(len(rows) // 2, 32)
+        xt = torch.from_numpy(x).to(dtype)
+        assert np.array_equal(xt.float().numpy(), x)
+        m = B.csa_fp4_quantize(xt.to(cuda), fmt="nvfp4", tensor_scale=torch.tensor([float(g)], device=cuda))
+        codes, sb = R.encode(x, "nvfp4", g)
+        assert np.array_equal(t2np(m.scales), R.block_scales(sb)), g
+        got = R.unpack(t2np(m.packed))
+        assert np.array_equal(got, codes), (float(g), np.argwhere(got != codes)[:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_encode_strided_rows_and_reused_buffers(B, cuda, dtype):
     big = torch.randn((3, 40, 200), device=cuda).to(dtype)
     x = big[:, 4:24, 8:136]  # inner rows 200 apart; the outer step is not 20 of them
