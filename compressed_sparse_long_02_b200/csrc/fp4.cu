@@ -14,8 +14,8 @@
 // flight before the first is used.  Rows and columns that pad a block get scale bytes of zero.
 //
 // All three kernels are bound by HBM: 2 or 4 bytes read and 17/32 or 9/16 written per element.
-// 8192 x 32768 bf16 on one B200: MXFP4 encoding 102 us (6.7 TB/s, the copy rate) and decoding 105;
-// NVFP4 113 us (6.1 TB/s: about 180 instructions for 16 values of a lane, MXFP4 160) and 106.
+// 8192 x 32768 bf16 on one B200: MXFP4 encoding 100 us (6.8 TB/s, the copy rate) and decoding 105;
+// NVFP4 112 us (6.2 TB/s: about 180 instructions for 16 values of a lane, MXFP4 160) and 106.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -286,9 +286,9 @@ Fp4Shape fp4_shape(bool nv, int64_t rows, int cols, int64_t ld, int chunk) {
   return p;
 }
 
-// One warp per task up to `per_sm` CTAs per SM, a loop beyond.  The encoder takes eight (four
-// run at once; NVFP4's set-up makes more CTAs dearer: 8192 x 32768 bf16 5% slower with 64),
-// the decoder as many as there are tasks up to 64 (that size: 119 us with 8, 114 with 16, 105 with 64).
+// One warp per task up to `per_sm` CTAs per SM (four run at once), a loop beyond.  Measured on 8192 x
+// 32768 (us; 8 / 16 / 64 per SM): MXFP4 from float32 183 / 182 / 172, from bf16 102 / 101 / 99.5; NVFP4,
+// whose warps have more to set up, 187 / 186 / 192 and 113 / 112 / 113; decoding to bf16 119 / 114 / 105.
 unsigned fp4_grid(int64_t n_tasks, int per_sm) {
   const int64_t blocks = (n_tasks + kFp4Threads / 32 - 1) / (kFp4Threads / 32);
   return static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms()) * per_sm));
@@ -325,7 +325,7 @@ cudaError_t launch_fp4_quantize(bool nv, const void* x, int in_bf16, int64_t row
                                 const float* tensor_scale, uint8_t* packed, uint8_t* scales, cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
   const Fp4Shape p = fp4_shape(nv, rows, cols, ld, in_bf16 ? kEncodeChunk<true> : kEncodeChunk<false>);
-  const unsigned grid = fp4_grid(p.n_rows32 * p.n_chunks, 8);
+  const unsigned grid = fp4_grid(p.n_rows32 * p.n_chunks, nv ? 16 : 64);
   auto k = nv ? (in_bf16 ? fp4_quantize_kernel<true, true> : fp4_quantize_kernel<false, true>)
               : (in_bf16 ? fp4_quantize_kernel<true, false> : fp4_quantize_kernel<false, false>);
   return launch_rows(k, grid, s, x, p, tensor_scale, packed, scales);
