@@ -158,6 +158,23 @@ def test_nvfp4_quotients_next_to_every_border(B, cuda, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g", [2.0 ** -98, 2.0 ** -60, (2.0 - 2.0 ** -23) * 2.0 ** -10, 1e-3, 2.0 ** 95])
+def test_nvfp4_extreme_scales_in_whole_row_blocks(B, cuda, dtype, g):
+    """Blocks whose scale is cut at 448 or underflows to 0, zero blocks and ordinary ones side by side in
+    whole and ragged row blocks, under tensor scales inside and outside the range of the common path."""
+    rng = np.random.default_rng(9)
+    rows, cols = 300, 1056
+    x = rng.standard_normal((rows, cols // 16, 16)) * 400 * g
+    x *= np.array([1.0, 2.0 ** 16, 2.0 ** -20, 0.0])[rng.choice(4, (rows, cols // 16), p=[0.7, 0.1, 0.1, 0.1])][..., None]
+    xt = torch.from_numpy(x.reshape(rows, cols).astype(np.float32)).to(dtype)
+    m = B.csa_fp4_quantize(xt.to(cuda), fmt="nvfp4", tensor_scale=torch.tensor([g], dtype=torch.float32, device=cuda))
+    codes, sb = R.encode(xt.float().numpy(), "nvfp4", g)
+    assert np.array_equal(t2np(m.scales), R.block_scales(sb))
+    got = R.unpack(t2np(m.packed))
+    assert np.array_equal(got, codes), np.argwhere(got != codes)[:4]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_encode_strided_rows_and_reused_buffers(B, cuda, dtype):
     big = torch.randn((3, 40, 200), device=cuda).to(dtype)
     x = big[:, 4:24, 8:136]  # inner rows 200 apart; the outer step is not 20 of them
@@ -232,6 +249,24 @@ def test_projection_is_its_four_steps(B, cuda, fmt, T, H, D, G, Rk, d):
     ref, mag = product(R.decode(codes, sb, fmt, None if zg is None else zg.item()), b64, 1)
     assert_product(y, ref, mag, G * Rk, torch.bfloat16, "projection")
     assert B.csa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,H,D,G,Rk,d", [(37, 16, 128, 4, 256, 512), (2100, 8, 64, 2, 640, 96)])
+@pytest.mark.parametrize("zg", [1e-6, 2.0 ** -98, (2.0 - 2.0 ** -23) * 2.0 ** -9, 2.0 ** 30])
+def test_projection_with_extreme_intermediate_scales(B, cuda, zg, T, H, D, G, Rk, d):
+    """z's scales cut at 448, out of the common path's range, all ones, or all zero: the projection still
+    equals its four steps, bit for bit."""
+    rng = np.random.default_rng(T)
+    o = torch.from_numpy(rng.standard_normal((T, H, D)).astype(np.float32)).to(cuda).to(torch.bfloat16)
+    A, _ = make(B, cuda, rng, G * Rk, H // G * D, "nvfp4", (H // G * D) ** -0.5)
+    Bm, _ = make(B, cuda, rng, d, G * Rk, "nvfp4", (G * Rk) ** -0.5)
+    og, zg = torch.tensor([6.0 / 2688], device=cuda), torch.tensor([zg], dtype=torch.float32, device=cuda)
+    y = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=og, z_scale=zg)
+    z = B.csa_fp4_linear(B.csa_fp4_quantize(o.reshape(T, -1), fmt="nvfp4", tensor_scale=og), A, groups=G)
+    zq = B.csa_fp4_quantize(z, fmt="nvfp4", tensor_scale=zg)
+    codes, sb = R.encode(z.float().cpu().numpy(), "nvfp4", zg.item())
+    assert np.array_equal(t2np(zq.scales), R.block_scales(sb)) and np.array_equal(R.unpack(t2np(zq.packed)), codes)
+    assert torch.equal(y, B.csa_fp4_linear(zq, Bm))
 
 
 def test_projection_reuses_its_workspace_on_any_stream(B, cuda):
