@@ -543,7 +543,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     for (int t = first; t < p.tiles; t += step, ++it) {
       const int buf = it % S::kAcc;
       const bool got = warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag);
-      if (!got && (kPair || p.splits > 1)) break;  // a lone CTA's warps meet below, whatever each saw
+      // warps that meet at barriers below leave together, whatever each saw (a wait may be given up just as
+      // it ends); an unsplit lone CTA's do so there
+      if constexpr (kPair && kOut != kOutF32) {
+        if (named_bar_or(1 + half, 128, !got)) break;
+      } else if (!got && (kPair || p.splits > 1)) {
+        break;
+      }
       tc_fence_after();
       int n0, g, m0;
       tile(t, n0, g, m0);
