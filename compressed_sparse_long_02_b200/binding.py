@@ -483,11 +483,13 @@ def _rows_2d(t: torch.Tensor, name: str):
     rows = t.numel() // cols if cols else 0
     if rows <= 1:
         return rows, cols, cols
-    ld, inner = 0, 1  # the step between rows, and the rows that the dimensions so far span
+    ld, inner = None, 1  # the step between rows (none yet), and the rows that the dimensions so far span
     for i in range(len(shape) - 2, -1, -1):
         if shape[i] > 1:
-            if ld == 0:
+            if ld is None:
                 ld = t.stride(i)
+                if ld < cols:  # an expanded dimension's stride is 0
+                    raise ValueError(f"{name}'s rows lie on one another")
             elif t.stride(i) != ld * inner:  # an outer dimension must continue the same spacing
                 raise ValueError(f"{name}'s rows are not evenly spaced")
         inner *= shape[i]

@@ -191,3 +191,45 @@ def test_refuses_more_rows_than_it_counts(B):
     assert L.csa_fp4_quantize(MX, P(16), BF16, rows, 64, 64, m, None) == UNSUPPORTED
     assert L.csa_fp4_dequantize(MX, m, rows, 64, BF16, P(16), 64, None) == UNSUPPORTED
     assert L.csa_fp4_pack_scales(MX, P(16), rows, 64, P(16), None) == UNSUPPORTED
+
+
+def test_rows_of_an_expanded_view_are_refused(B):
+    """A stride of 0 in any dimension longer than 1 (inside, between, outside), or rows that overlap, names
+    fewer rows than it counts: refused, since a call would read or write past the storage."""
+    base = torch.zeros((4, 64))
+    for t in (base[:, None].expand(4, 3, 64),                         # the inner row dimension
+              torch.zeros((2, 1, 64)).expand(2, 3, 64),
+              torch.zeros((2, 1, 4, 64)).expand(2, 5, 4, 64),         # between
+              torch.zeros((1, 4, 64)).expand(3, 4, 64),               # the outer one
+              torch.zeros((1, 1, 64)).expand(3, 4, 64),               # all of them
+              torch.zeros((1, 64)).expand(5, 64), torch.zeros(64).expand(5, 64),
+              torch.zeros(64).as_strided((2, 3, 16), (0, 16, 1)),
+              torch.zeros(256).as_strided((5, 64), (32, 1))):         # rows half on one another
+        with pytest.raises(ValueError):
+            B._rows_2d(t, "x")
+    # dimensions of one element may have any stride
+    assert B._rows_2d(base.as_strided((1, 4, 64), (0, 64, 1)), "x") == (4, 64, 64)
+    assert B._rows_2d(base.as_strided((4, 1, 64), (64, 0, 1)), "x") == (4, 64, 64)
+    assert B._rows_2d(base[:1].as_strided((1, 1, 64), (0, 0, 1)), "x") == (1, 64, 64)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_rows_of_any_view_stay_in_its_storage(B, seed):
+    """Whatever view is taken as evenly spaced rows, the rows so described are the view's, in order."""
+    rng = np.random.default_rng(seed)
+    taken = 0
+    for _ in range(400):
+        nd = int(rng.integers(1, 5))
+        shape = [int(v) for v in rng.integers(1, 4, nd - 1)] + [8]
+        stride = [int(v) for v in rng.choice([0, 4, 8, 16, 24, 32, 48, 64, 96, 144], nd - 1)] + [1]
+        size = 1 + sum((n - 1) * s for n, s in zip(shape, stride))
+        base = torch.arange(size)
+        t = base.as_strided(shape, stride)
+        try:
+            rows, cols, ld = B._rows_2d(t, "x")
+        except ValueError:
+            continue
+        taken += 1
+        assert rows * cols == t.numel() and (rows - 1) * ld + cols <= size
+        assert torch.equal(base.as_strided((rows, cols), (ld, 1)), t.reshape(rows, cols))
+    assert taken > 40
