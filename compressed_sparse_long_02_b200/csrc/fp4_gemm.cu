@@ -249,6 +249,17 @@ __device__ __forceinline__ void encode_row(const float (&o)[4], int m, int feat,
   if (feat % kBlk == 0) p.z_scale[scale_at(m, feat / kBlk, n_atoms)] = static_cast<uint8_t>(byte);
 }
 
+// The tensor scales of a product where gx gw is no normal float32: gx gw = pre alpha, pre a power of two
+// and alpha normal, so that y = (sum pre) alpha rounds once.  A sum is 0 or in [2^-20, 2^53] (terms are
+// multiples of (2^-1 2^-9)^2, at most (6 448)^2, and at most 2^30 of them), so sum pre is exact for pre in
+// [2^-100, 2^70]; past either end every result is 0 or infinite as it should be, and a sum of 0 stays 0.
+static __device__ __noinline__ float2 wide_scales(float gx, float gw) {
+  int ex, ew;
+  const float m = frexpf(gx, &ex) * frexpf(gw, &ew);  // in [1/4, 1)
+  const int e = ex + ew, ea = max(-124, min(e, 127));
+  return make_float2(ldexpf(m, ea), ldexpf(1.f, max(-100, min(e - ea, 70))));
+}
+
 template <bool kNv, int kBN, int kOut>
 __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -530,7 +541,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     const int quarter = warp & 3, half = (warp - kOutWarp) >> 2;
     constexpr int kHalf = kBN / 2;
     const int f = 32 * quarter + lane, c0 = half * kHalf;  // this lane's feature, this warp's first token of a tile
-    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+    float alpha = 1.f, pre = 1.f;  // see wide_scales
+    if constexpr (kNv) {
+      const float gx = p.gx ? __ldg(p.gx) : 1.f, gw = p.gw ? __ldg(p.gw) : 1.f;
+      alpha = gx * gw;
+      if (!(alpha >= 0x1p-126f && alpha < INFINITY) && gx > 0.f && gw > 0.f && gx < INFINITY && gw < INFINITY) {
+        const float2 f = wide_scales(gx, gw);
+        alpha = f.x, pre = f.y;
+      }
+    }
+    const bool wide = kNv && pre != 1.f;
     const NvScale nvz(kOut == kOutFp4 && kNv ? __ldg(p.gz) : 1.f);
     const uint32_t acc_done = kPair ? dsmem_map(acc_empty, 0) : 0u;
     if (!kPair && p.splits > 1 && warp == kOutWarp && lane == 0) {  // the bytes this CTA will receive
@@ -597,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
             const float4 q = *reinterpret_cast<const float4*>(part + r * cap * kTileN);
             sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
           }
+          if (wide) sum.x *= pre, sum.y *= pre, sum.z *= pre, sum.w *= pre;
           const float o[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
           const int m = m0 + tok0 + i, n = n0 + 4 * lane;
           const int64_t at = static_cast<int64_t>(m) * p.ldy + static_cast<int64_t>(g) * p.N + n;
@@ -622,6 +643,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         for (int c = 0; c < kHalf; c += 16) tmem_ld16(src + c, v + c);
         tmem_wait_ld();
         release();
+        if (wide) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * pre);
+        }
         if (n < p.N) {
 #pragma unroll
           for (int i = 0; i < kHalf; ++i) {
@@ -639,6 +664,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           tmem_ld_16x256b_x4(src + c, u[0]);
           tmem_ld_16x256b_x4(src + (16u << 16) + c, u[1]);
           tmem_wait_ld();
+          if (wide) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i / 16][i % 16] = __float_as_uint(__uint_as_float(u[i / 16][i % 16]) * pre);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
 #pragma unroll

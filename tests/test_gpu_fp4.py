@@ -427,3 +427,80 @@ print("captured ok")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
+
+
+def rescaled(m, v, g):
+    """The same codes and block scales under the tensor scale g, and the float64 values."""
+    g0 = float(m.tensor_scale.item())
+    g = np.float32(g)
+    return m._replace(tensor_scale=torch.full_like(m.tensor_scale, float(g))), v / g0 * float(g)
+
+
+def small_sums(B, dev, rng, rows, cols):
+    """Random codes under the smallest block scale, 2^-9: products of sums far below 1."""
+    codes = rng.integers(0, 16, (rows, cols)).astype(np.uint8)
+    sb = np.ones((rows, cols // 16), np.uint8)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    m = B.Fp4Matrix("nvfp4", rows, cols, up(R.pack(codes)), up(R.block_scales(sb)), torch.ones(1, device=dev))
+    return m, R.decode(codes, sb, "nvfp4", 1.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 130, 512), (3, 257, 4096), (40, 200, 2080), (300, 1001, 288), (1700, 1301, 288), (2000, 512, 256)])
+@pytest.mark.parametrize("gx,gw,small", [(2.0 ** -80, 2.0 ** -75, False), (1e-22, 1e-22, False), (2.0 ** -98, 2.0 ** -40, False),
+                                         (2.0 ** -149, 2.0 ** 60, False), (2.0 ** -149, 2.0 ** -149, False),
+                                         (2.0 ** 95, 2.0 ** 37, True), (2.0 ** 70, 2.0 ** 60, True), (2.0 ** 127, 2.0 ** 127, True),
+                                         (2.0 ** 127, 2.0 ** -149, False)])
+def test_product_of_extreme_tensor_scales(B, cuda, M, N, K, gx, gw, small):
+    """Tensor scales whose product leaves float32's normal range, or just about: results that float32 can hold
+    are right, others are 0 or infinite, and rows of zeros give zeros.  The bound is assert_product's, and half a
+    step of the subnormals (of float32, and of the type rounded to)."""
+    rng = np.random.default_rng(M + N + K)
+    build = (lambda r, std: small_sums(B, cuda, rng, r, K)) if small else (lambda r, std: make(B, cuda, rng, r, K, "nvfp4", std))
+    (mx, x), (mw, w) = rescaled(*build(M, 1.0), gx), rescaled(*build(N, K ** -0.5), gw)
+    mx.packed[M // 2] = 0
+    mw.packed[N // 3] = 0
+    x[M // 2], w[N // 3] = 0.0, 0.0
+    ref, mag = product(x, w, 1)
+    for dtype, sub in ((torch.float32, 2.0 ** -150), (torch.bfloat16, 2.0 ** -134)):
+        y = B.csa_fp4_linear(mx, mw, out_dtype=dtype)
+        assert B.csa_get_device_error() == 0
+        y = y.double().cpu().numpy()
+        assert not y[M // 2].any() and not y[:, N // 3].any()
+        tol = ((-(-K // 64) + 8) * 2.0 ** -23 + 4 * 2.0 ** -24) * mag + torch.finfo(dtype).eps / 2 * np.abs(ref) + sub + 2.0 ** -150
+        over = np.abs(ref) + tol > torch.finfo(dtype).max  # may be infinite
+        must = np.abs(ref) - tol > 2.0 ** 128              # has to be
+        with np.errstate(invalid="ignore"):
+            near = np.abs(y - ref) <= tol
+        assert np.where(must, np.isinf(y) & (np.sign(y) == np.sign(ref)), near | (over & np.isinf(y))).all()
+        if M > 1 and max(gx, gw) < 2.0 ** 100 and min(gx, gw) > 2.0 ** -100:  # (of one row, it is the one of zeros)
+            assert (near & (ref != 0)).any() and y.any()   # there are results to be right about
+
+
+@pytest.mark.parametrize("T,H,D,G,Rk,d", [(37, 16, 128, 4, 256, 512), (2100, 8, 64, 2, 640, 96)])
+def test_projection_between_extreme_scales(B, cuda, T, H, D, G, Rk, d):
+    """o and A so small that o_scale times A's scale is no normal float32, z's tensor scale subnormal and Bm's
+    large: y is right against the reference's encoding of z, and z against the reference's product."""
+    rng = np.random.default_rng(T)
+    o = torch.from_numpy((rng.standard_normal((T, H, D)) * 2.0 ** -70).astype(np.float32)).to(cuda).to(torch.bfloat16)
+    A, a64 = rescaled(*make(B, cuda, rng, G * Rk, H // G * D, "nvfp4"), 2.0 ** -66)
+    Bm, b64 = rescaled(*make(B, cuda, rng, d, G * Rk, "nvfp4"), 2.0 ** 50)
+    one = lambda v: torch.tensor([v], dtype=torch.float32, device=cuda)  # noqa: E731
+    og = one(2.0 ** -67 / 2688)
+    oq = B.csa_fp4_quantize(o.reshape(T, -1), fmt="nvfp4", tensor_scale=og)
+    codes, sb = R.encode(o.float().cpu().numpy().reshape(T, -1), "nvfp4", og.item())
+    assert np.array_equal(R.unpack(t2np(oq.packed)), codes)
+    o64 = R.decode(codes, sb, "nvfp4", og.item())
+    z = B.csa_fp4_linear(oq, A, groups=G)
+    zref, zmag = product(o64, a64, G)
+    K = H // G * D
+    tol = ((-(-K // 64) + 8) * 2.0 ** -23 + 4 * 2.0 ** -24) * zmag + 2.0 ** -8 * np.abs(zref) + 2.0 ** -134 + 2.0 ** -150
+    zf = z.double().cpu().numpy()
+    assert zf.any() and (np.abs(zf - zref) <= tol).all()
+    zg = one(float(np.abs(zf).max() / 2688))
+    assert 0 < zg.item() < 2.0 ** -126 and og.item() * 2.0 ** -66 < 2.0 ** -126
+    y = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=og, z_scale=zg)
+    codes, sb = R.encode(z.float().cpu().numpy(), "nvfp4", zg.item())
+    ref, mag = product(R.decode(codes, sb, "nvfp4", zg.item()), b64, 1)
+    assert np.abs(ref).max() > 2.0 ** -110
+    assert_product(y, ref, mag, G * Rk, torch.bfloat16, "projection")
+    assert B.csa_get_device_error() == 0
