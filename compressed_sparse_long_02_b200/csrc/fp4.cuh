@@ -65,9 +65,11 @@ struct NvScale {
     rcp = __frcp_rn(six_g);
   }
   // scale byte of a block: e4m3(amax / (6 g)), to nearest even, at most 448 (amax is cut at 1024 times
-  // 6 g, far beyond; quotients too small for an exact residual are 0 in e4m3 anyway)
+  // 6 g, far beyond; quotients too small for an exact residual are 0 in e4m3 anyway); 0 / 0, a block of zeros
+  // under g = 0 (which a tensor of zeros has for its largest value / 2688), counts as 0
   __device__ __forceinline__ uint32_t byte(float amax) const {
-    const float q = div_range(six_g) ? div_given_rcp(fminf(amax, 1024.f * six_g), six_g, rcp) : __fdiv_rn(amax, six_g);
+    const float q = div_range(six_g) ? div_given_rcp(fminf(amax, 1024.f * six_g), six_g, rcp)
+                                     : fmaxf(__fdiv_rn(amax, six_g), 0.f);
     return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
   }
 };

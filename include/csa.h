@@ -379,14 +379,15 @@ CSA_API csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d
  * and at most 2^30 (rows at most 2^40), is
  *   packed        uint8 [rows, cols/2]: E2M1 codes, element 2i in the low nibble of byte i;
  *   scales        uint8, one per block of a row's consecutive elements, in the layout below;
- *   tensor_scale  device float32, one value g > 0 (NVFP4), or NULL (MXFP4: g = 1).
+ *   tensor_scale  device float32, one value g >= 0 (NVFP4; with 0 every value is held as 0), or
+ *                 NULL (MXFP4: g = 1).
  *
  * CSA_MXFP4: blocks of 32, the codes and UE8M0 scales of csa_quantize_mxfp4; value = code * 2^E.
  * CSA_NVFP4: blocks of 16, E4M3 scales; value = code * s * g.  Encoding, every step rounded once
  *   to float32: s = e4m3(amax / (6 g)) (to nearest even, at most 448), T = s g,
- *   code = e2m1(x / T) (to nearest even, at most 6; 0 when T = 0).
- * In both a NaN is left out of amax and encoded as +6, and an infinity counts as 2^128 in amax
- * (E = 126; s = 448) and is encoded as +-6.
+ *   code = e2m1(x / T) (to nearest even, at most 6; 0 when T = 0); s = 0 in a block of zeros.
+ * In both a NaN is left out of amax and encoded as +6 (0 when T = 0), and an infinity counts as
+ * 2^128 in amax (E = 126; s = 448) and is encoded as +-6.
  *
  * Scale layout: rows in blocks of 128, a row's scales in atoms of 4; atom (row block i, atom a) is
  * the 512 bytes at ((i * n_atoms) + a) * 512, n_atoms = ceil(cols / (4 * block)), and its scale

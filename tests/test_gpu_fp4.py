@@ -504,3 +504,43 @@ def test_projection_between_extreme_scales(B, cuda, T, H, D, G, Rk, d):
     assert np.abs(ref).max() > 2.0 ** -110
     assert_product(y, ref, mag, G * Rk, torch.bfloat16, "projection")
     assert B.csa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tensors_of_zeros(B, cuda, dtype):
+    """A tensor of zeros under the tensor scale that its largest value gives, 0: bytes, values and products of
+    zeros; a tensor scale of 0 makes zeros of any values."""
+    for rows, cols in ((1, 32), (300, 1056)):
+        x = torch.zeros((rows, cols), dtype=dtype, device=cuda)
+        x[rows // 2] = -0.0
+        g = (x.abs().amax() / 2688).float().reshape(1)
+        m = B.csa_fp4_quantize(x, fmt="nvfp4", tensor_scale=g)
+        assert g.item() == 0 and not m.packed.any() and not m.scales.any()
+        assert not B.csa_fp4_dequantize(m, dtype=torch.float32).any()
+        x = torch.randn((rows, cols), device=cuda).to(dtype)
+        x[0, :3] = torch.tensor([float("nan"), float("inf"), -float("inf")])
+        m0 = B.csa_fp4_quantize(x, fmt="nvfp4", tensor_scale=g)
+        assert not m0.packed.any() and not B.csa_fp4_dequantize(m0, dtype=torch.float32).any()
+        rng = np.random.default_rng(cols)
+        w, _ = make(B, cuda, rng, 2000, cols, "nvfp4")  # lone tiles or pairs by the rows
+        big, _ = make(B, cuda, rng, 2100, cols, "nvfp4")
+        for out in (torch.float32, torch.bfloat16):
+            for a, b in ((m, w), (m0, w), (big, m), (big, m0), (m, m0)):
+                assert not B.csa_fp4_linear(a, b, out_dtype=out).any()
+
+
+@pytest.mark.parametrize("T,H,D,G,Rk,d", [(1, 16, 128, 4, 256, 512), (37, 16, 128, 4, 256, 512), (2100, 8, 64, 2, 640, 96)])
+def test_projection_of_zeros(B, cuda, T, H, D, G, Rk, d):
+    """o of zeros under o_scale 0, and an intermediate of zeros under z_scale 0, give zeros."""
+    rng = np.random.default_rng(T)
+    A, _ = make(B, cuda, rng, G * Rk, H // G * D, "nvfp4")
+    Bm, _ = make(B, cuda, rng, d, G * Rk, "nvfp4")
+    zero, one = torch.zeros(1, device=cuda), torch.full((1,), 6.0 / 2688, device=cuda)
+    o = torch.zeros((T, H, D), dtype=torch.bfloat16, device=cuda)
+    for og, zg in ((zero, zero), (zero, one), (one, zero), (one, one)):
+        y = B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=og, z_scale=zg)
+        assert not y.any(), (og.item(), zg.item())
+    o = torch.randn((T, H, D), device=cuda).to(torch.bfloat16)
+    assert not B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=one, z_scale=zero).any()
+    assert not B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=zero, z_scale=one).any()
+    assert B.csa_get_device_error() == 0
