@@ -569,8 +569,8 @@ static csa_status fp4_product_status(int64_t M, int64_t N, int64_t K, int64_t G)
   return CSA_OK;
 }
 
-csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x, const csa_fp4_mat* w,
-                          csa_dtype y_dtype, void* y, int64_t ldy, cudaStream_t stream) {
+static csa_status fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x, const csa_fp4_mat* w,
+                             csa_dtype y_dtype, void* y, int64_t ldy, int starve, int starve_ranks, cudaStream_t stream) {
   if (!fp4_format_ok(fmt) || (y_dtype != CSA_F32 && y_dtype != CSA_BF16)) return CSA_ERR_INVALID_ARG;
   csa_status st = fp4_product_status(M, N, K, G);
   if (st != CSA_OK) return st;
@@ -594,7 +594,22 @@ csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const 
   a.out_bf16 = y_dtype == CSA_BF16;
   a.y = y;
   a.ldy = ldy;
+  a.starve = starve;
+  a.starve_ranks = starve_ranks;
   return from_cuda(launch_fp4_linear(a, stream));
+}
+
+csa_status csa_fp4_linear(csa_fp4_format fmt, int M, int N, int K, int G, const csa_fp4_mat* x, const csa_fp4_mat* w,
+                          csa_dtype y_dtype, void* y, int64_t ldy, cudaStream_t stream) {
+  return fp4_linear(fmt, M, N, K, G, x, w, y_dtype, y, ldy, 0, 0, stream);
+}
+
+csa_status csa_selftest_fp4_give_up(int barrier, int ranks, csa_fp4_format fmt, int M, int N, int K, int G,
+                                    const csa_fp4_mat* x, const csa_fp4_mat* w, csa_dtype y_dtype, void* y, int64_t ldy,
+                                    cudaStream_t stream) {
+  if (barrier < 1 || barrier > 7 || ranks < 1 || ranks > 255) return CSA_ERR_INVALID_ARG;
+  if ((fmt == CSA_NVFP4) != (y_dtype == CSA_F32)) return CSA_ERR_UNSUPPORTED;
+  return fp4_linear(fmt, M, N, K, G, x, w, y_dtype, y, ldy, barrier, ranks, stream);
 }
 
 size_t csa_grouped_out_proj_fp4_workspace(csa_fp4_format fmt, int T, int H, int D, int G, int R) {

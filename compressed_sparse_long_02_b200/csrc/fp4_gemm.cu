@@ -102,6 +102,7 @@ struct LinearParams {
   int n_blocks, m_blocks, tiles, splits;
   int x_atoms, w_atoms;   // scale atoms per row block of X and W
   int x_group_atoms;      // atoms of one group's K columns of X
+  int starve;             // kStarve: the barrier, and above 4 bits a bit for each CTA of a cluster in which
   const float* gx;
   const float* gw;
   void* y;
@@ -114,6 +115,9 @@ struct LinearParams {
   int z_atoms;
   int32_t* err;
 };
+
+// (with the seven tensor maps 1024 bytes of parameters: past that a launch took 0.1 us longer)
+static_assert(sizeof(LinearParams) <= 128, "parameters");
 
 template <int kOut>
 __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
@@ -260,7 +264,9 @@ static __device__ __noinline__ float2 wide_scales(float gx, float gw) {
   return make_float2(ldexpf(m, ea), ldexpf(1.f, max(-100, min(e - ea, 70))));
 }
 
-template <bool kNv, int kBN, int kOut>
+// kStarve: a barrier waits for an arrival that never comes, and the limit of a wait is 0.1 s
+// (csa_selftest_fp4_give_up).
+template <bool kNv, int kBN, int kOut, bool kStarve>
 __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     fp4_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_xt, const __grid_constant__ CUtensorMap tm_wt,
@@ -284,26 +290,32 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   uint64_t* fin = recv_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* loads = abort_flag + 1;  // of a pair: slabs that this CTA loaded, (in the leader) that the other
+  volatile int* peer_loads = loads + 1;  // one did, and whether the other one gave up
+  volatile int* peer_abort = loads + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // CTA of the cluster: half of the tile's features in a pair, a share of K otherwise
   const int per_tile = kPair ? 2 : p.splits;
   const int rank = static_cast<int>(blockIdx.x) % per_tile;
   const bool leader = !kPair || rank == 0;
+  constexpr long long wait_limit = kStarve ? kWaitLimitCycles / 20 : kWaitLimitCycles;  // cycles that a role waits
 
   if (threadIdx.x == 0) {
+    const int starved = kStarve && (p.starve >> (4 + rank) & 1) ? p.starve & 15 : 0;
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&sf_full[s], 1);
-      mbar_init(&sf_ready[s], 4 * S::kCtas);
+      mbar_init(&full[s], 1 + (starved == 1));
+      mbar_init(&empty[s], 1 + (starved == 2));
+      mbar_init(&sf_full[s], 1 + (starved == 3));
+      mbar_init(&sf_ready[s], 4 * S::kCtas + (starved == 4));
     }
     for (int b = 0; b < S::kAcc; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8 * S::kCtas);
+      mbar_init(&acc_full[b], 1 + (starved == 5));
+      mbar_init(&acc_empty[b], 8 * S::kCtas + (starved == 6));
     }
-    mbar_init(recv_full, 1);
+    mbar_init(recv_full, 1 + (starved == 7));
     mbar_init(fin, 1);
     *abort_flag = 0;
+    if constexpr (kPair) *peer_abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_x);
     prefetch_tmap(&tm_w);
@@ -380,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           const int w_sf = w_row / 128 * p.w_atoms, x_sf = m0 / 128 * p.x_atoms + g * p.x_group_atoms;
           for (int sl = slab0; sl < slab1; ++sl, ++j) {
             const int st = j % S::kStages;
-            if (!mbar_wait(&empty[st], ((j / S::kStages) & 1) ^ 1, p.err, abort_flag)) {
+            if (!mbar_wait(&empty[st], ((j / S::kStages) & 1) ^ 1, p.err, abort_flag, wait_limit)) {
               ok = false;
               break;
             }
@@ -405,11 +417,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           }
         }
         // the last loads issued must have landed before shared memory is reused or freed (of a pair: the
-        // leader waits for both CTAs' bytes, and the other CTA for the leader at the end)
-        volatile int never = 0;
+        // leader waits for both CTAs' bytes, and the other CTA for the leader at the end); one limit for all
+        const long long t_end = clock64() + wait_limit;
         for (int i = std::max(0, j - S::kStages); i < j; ++i) {
-          mbar_wait(&sf_full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
-          if (leader) mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, p.err, &never);
+          mbar_wait_until(&sf_full[i % S::kStages], (i / S::kStages) & 1, p.err, t_end);
+          if (leader) mbar_wait_until(&full[i % S::kStages], (i / S::kStages) & 1, p.err, t_end);
+        }
+        if constexpr (kPair) {
+          *loads = j;
+          if (!leader) dsmem_st(dsmem_map(const_cast<int*>(peer_loads), 0), j);
         }
       }
       __syncwarp();
@@ -423,13 +439,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
         bool ok = true;
         for (int t = first; ok && t < p.tiles; t += step, ++it) {
           const int buf = it % S::kAcc;
-          if (!warp_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag)) break;
+          if (!warp_wait(&acc_empty[buf], ((it / S::kAcc) & 1) ^ 1, p.err, abort_flag, wait_limit)) break;
           tc_fence_after();
           const uint32_t acc = tmem + kBN * buf;
           for (int sl = slab0; sl < slab1; ++sl, ++j) {
             const int st = j % S::kStages;
             const uint32_t ph = (j / S::kStages) & 1;
-            if (!warp_wait(&sf_ready[st], ph, p.err, abort_flag) || !warp_wait(&full[st], ph, p.err, abort_flag)) {
+            if (!warp_wait(&sf_ready[st], ph, p.err, abort_flag, wait_limit) ||
+                !warp_wait(&full[st], ph, p.err, abort_flag, wait_limit)) {
               ok = false;
               break;
             }
@@ -471,14 +488,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           }
         }
         if (elect_one()) {
-          if constexpr (kPair)
-            tc_commit_pair_local(fin);
-          else
-            tc_commit(fin);
+          commit(fin);  // (of a pair: in both CTAs, after the commits that arrived on the other's barriers)
         }
         __syncwarp();
-        volatile int never = 0;
-        mbar_wait(fin, 0, p.err, &never);
+        mbar_wait_until(fin, 0, p.err, clock64() + wait_limit);
       }
       __syncwarp();
     }
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
       tile(t, n0, g, m0);
       for (int sl = slab0; sl < slab1; ++sl, ++j) {
         const int st = j % S::kStages;
-        if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag)) {
+        if (!warp_wait(&sf_full[st], (j / S::kStages) & 1, p.err, abort_flag, wait_limit)) {
           ok = false;
           break;
         }
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
     int it = 0;
     for (int t = first; t < p.tiles; t += step, ++it) {
       const int buf = it % S::kAcc;
-      const bool got = warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag);
+      const bool got = warp_wait_sleep(&acc_full[buf], (it / S::kAcc) & 1, p.err, abort_flag, wait_limit);
       // warps that meet at barriers below leave together, whatever each saw (a wait may be given up just as
       // it ends); an unsplit lone CTA's do so there
       if constexpr (kPair && kOut != kOutF32) {
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
           }
         }
         release();
-        if (p.splits == 1 ? named_bar_or(1, 256, !got) : !warp_wait(recv_full, 0, p.err, abort_flag)) break;
+        if (p.splits == 1 ? named_bar_or(1, 256, !got) : !warp_wait(recv_full, 0, p.err, abort_flag, wait_limit)) break;
         // a warp takes a token at a time: four features per lane, the partials added in rank order
         const int tok0 = p.splits > 1 ? rank * cap : 0, n_tok = p.splits > 1 ? min(cap, m_valid - rank * cap) : m_valid;
         for (int i = warp - kOutWarp; i < n_tok; i += 8) {
@@ -737,7 +750,34 @@ __global__ void __launch_bounds__(kThreads, Shape<kNv, kBN, kOut>::kMinBlocks)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync_all();  // neither CTA leaves while the other's MMAs or loads use it
+  // nor, having given up, while those sent to it may be on their way
+  if (!kPair && p.splits > 1 && warp == kOutWarp && *abort_flag) mbar_wait_until(recv_full, 0, p.err, clock64() + wait_limit);
+  if constexpr (kPair) {
+    if (warp == 1 && !leader) {
+      mbar_wait_until(fin, 0, p.err, clock64() + wait_limit);
+      __syncwarp();
+    }
+    if (threadIdx.x == 0 && *abort_flag) dsmem_st(dsmem_map(const_cast<int*>(peer_abort), rank ^ 1), 1);
+    __syncwarp();
+    cluster_sync_all();  // neither CTA leaves while the other's MMAs or loads use it
+    if (*abort_flag || *peer_abort) {
+      // the other CTA may have gone further than the leader and loaded slabs whose bytes the leader never
+      // announced (at most a ring of them): it does so now, and waits for them
+      if (leader && threadIdx.x == 0) {
+        const int j0 = *loads, j1 = *peer_loads;
+        for (int j = j0; j < j1; ++j) {
+          int n0, g, m0;
+          tile(first + j / slabs * step, n0, g, m0);
+          const int rows = max(0, min(kTileN, p.N - n0 - kTileN)) + max(0, min(S::kRowsX, p.M - m0 - S::kRowsX));
+          mbar_arrive_expect_tx(&full[j % S::kStages], rows * kSlabBytes);
+        }
+        const long long t_end = clock64() + wait_limit;
+        for (int j = j0; j < j1; ++j) mbar_wait_until(&full[j % S::kStages], (j / S::kStages) & 1, p.err, t_end);
+      }
+      __syncwarp();
+      cluster_sync_all();
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (kPair)
@@ -766,7 +806,7 @@ int resident_clusters(K k, size_t smem, int size) {
   return cudaOccupancyMaxActiveClusters(&n, k, &cfg) == cudaSuccess && n > 0 ? n : num_sms() / size;
 }
 
-template <bool kNv, int kBN, int kOut>
+template <bool kNv, int kBN, int kOut, bool kStarve>
 cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cudaStream_t s) {
   using Sh = Shape<kNv, kBN, kOut>;
   static int smem_set[64], resident[64];  // pairs: what runs at once, per device
@@ -787,7 +827,7 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
   const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_blocks * a.G;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   p.tiles = static_cast<int>(tiles);
-  auto k = fp4_linear_kernel<kNv, kBN, kOut>;
+  auto k = fp4_linear_kernel<kNv, kBN, kOut, kStarve>;
   const cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(k), Sh::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   const dim3 block(kThreads);
@@ -858,7 +898,7 @@ cudaError_t lone_residents(const int (**out)[2][4]) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   *out = &table[dev];
   if (table[dev][1][3] != 0) return cudaSuccess;
-  const auto narrow = fp4_linear_kernel<kNv, 32, kOut>, wide = fp4_linear_kernel<kNv, 128, kOut>;
+  const auto narrow = fp4_linear_kernel<kNv, 32, kOut, false>, wide = fp4_linear_kernel<kNv, 128, kOut, false>;
   constexpr size_t narrow_smem = Shape<kNv, 32, kOut>::kSmem, wide_smem = Shape<kNv, 128, kOut>::kSmem;
   cudaError_t e = set_dyn_smem(reinterpret_cast<const void*>(narrow), narrow_smem, smem_set[0]);
   if (e == cudaSuccess) e = set_dyn_smem(reinterpret_cast<const void*>(wide), wide_smem, smem_set[1]);
@@ -870,17 +910,17 @@ cudaError_t lone_residents(const int (**out)[2][4]) {
   return cudaSuccess;
 }
 
-template <bool kNv, int kOut>
+template <bool kNv, int kOut, bool kStarve = false>
 cudaError_t launch_shape(const Fp4LinearArgs& a, LinearParams& p, cudaStream_t s) {
   const int(*resident)[2][4] = nullptr;
   const cudaError_t e = lone_residents<kNv, kOut>(&resident);
   if (e != cudaSuccess) return e;
   const Choice c = choose(a, *resident);
   switch (c.tokens) {
-    case 32: return launch_tile<kNv, 32, kOut>(a, p, c.splits, s);
-    case 64: return launch_tile<kNv, 64, kOut>(a, p, c.splits, s);
-    case 128: return launch_tile<kNv, 128, kOut>(a, p, c.splits, s);
-    default: return launch_tile<kNv, 256, kOut>(a, p, 1, s);
+    case 32: return launch_tile<kNv, 32, kOut, kStarve>(a, p, c.splits, s);
+    case 64: return launch_tile<kNv, 64, kOut, kStarve>(a, p, c.splits, s);
+    case 128: return launch_tile<kNv, 128, kOut, kStarve>(a, p, c.splits, s);
+    default: return launch_tile<kNv, 256, kOut, kStarve>(a, p, 1, s);
   }
 }
 
@@ -907,6 +947,10 @@ cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s) {
   p.z_atoms = fp4_atoms(a.nv, a.G * a.N);
   p.err = device_error_word();
   if (p.err == nullptr) return cudaErrorUnknown;
+  if (a.starve != 0) {
+    p.starve = a.starve | a.starve_ranks << 4;
+    return a.nv ? launch_shape<true, kOutF32, true>(a, p, s) : launch_shape<false, kOutBf16, true>(a, p, s);
+  }
   if (a.z_packed != nullptr) return a.nv ? launch_shape<true, kOutFp4>(a, p, s) : launch_shape<false, kOutFp4>(a, p, s);
   if (a.nv) return a.out_bf16 ? launch_shape<true, kOutBf16>(a, p, s) : launch_shape<true, kOutF32>(a, p, s);
   return a.out_bf16 ? launch_shape<false, kOutBf16>(a, p, s) : launch_shape<false, kOutF32>(a, p, s);

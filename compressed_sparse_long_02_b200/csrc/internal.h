@@ -136,6 +136,7 @@ struct Fp4LinearArgs {
   uint8_t* z_packed;        // non-null: the result is rounded to bf16 and encoded instead (N a
   uint8_t* z_scale;         // multiple of 128): codes [M, G N / 2], scales, tensor scale
   const float* gz;
+  int starve, starve_ranks; // csa_selftest_fp4_give_up (MXFP4 to bf16, NVFP4 to float32), else 0
 };
 cudaError_t launch_fp4_linear(const Fp4LinearArgs& a, cudaStream_t s);
 

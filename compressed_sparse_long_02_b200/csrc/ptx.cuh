@@ -92,19 +92,32 @@ __device__ __forceinline__ bool mbar_test(const uint64_t* bar, uint32_t parity) 
 // Bounded wait for the phase of `bar` with parity `parity` to complete.
 // `abort_flag` (shared) lets the first role that times out release the others.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_t* err,
-                                          volatile int* abort_flag) {
+                                          volatile int* abort_flag, long long limit = kWaitLimitCycles) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(a, parity)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       atomicExch(err, CSA_DEVERR_TIMEOUT);
       *abort_flag = 1;
       return false;
     }
   }
+}
+
+// The same until clock64() passes t_end, whatever an abort flag says: for what is in flight and has to
+// land before its shared memory is left (several such waits share one t_end).
+__device__ __forceinline__ bool mbar_wait_until(uint64_t* bar, uint32_t parity, int32_t* err, long long t_end) {
+  const uint32_t a = smem_u32(bar);
+  while (!mbar_try_wait(a, parity)) {
+    if (clock64() > t_end) {
+      atomicExch(err, CSA_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // The same wait for roles with many waiting warps: try_wait carries a suspend-time hint,
@@ -123,14 +136,14 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
   return ok != 0;
 }
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, int32_t* err,
-                                                volatile int* abort_flag) {
+                                                volatile int* abort_flag, long long limit = kWaitLimitCycles) {
   const uint32_t a = smem_u32(bar);
   if (mbar_try_wait_sleep(a, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait_sleep(a, parity)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       atomicExch(err, CSA_DEVERR_TIMEOUT);
       *abort_flag = 1;
       return false;
@@ -138,15 +151,16 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
   }
 }
 __device__ __forceinline__ bool warp_wait_sleep(uint64_t* bar, uint32_t parity, int32_t* err,
-                                                volatile int* abort_flag) {
-  const bool ok = mbar_wait_sleep(bar, parity, err, abort_flag);
+                                                volatile int* abort_flag, long long limit = kWaitLimitCycles) {
+  const bool ok = mbar_wait_sleep(bar, parity, err, abort_flag, limit);
   return __all_sync(0xffffffffu, ok);
 }
 
 // All 32 lanes wait; every lane gets the same answer (false if any lane gave up), so
 // the warp stays converged for the collectives that follow.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, err, abort_flag);
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort_flag,
+                                          long long limit = kWaitLimitCycles) {
+  const bool ok = mbar_wait(bar, parity, err, abort_flag, limit);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -393,11 +407,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// the same on this CTA's barrier only
-__device__ __forceinline__ void tc_commit_pair_local(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate, uint32_t sfa_tmem, uint32_t sfb_tmem) {
   asm volatile(
@@ -516,6 +525,10 @@ __device__ __forceinline__ uint4 dsmem_ld4(uint32_t addr) {  // 16-byte aligned
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr));
   return v;
+}
+
+__device__ __forceinline__ void dsmem_st(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Asynchronous store of a word into a CTA of the cluster (shared::cluster addresses); its four

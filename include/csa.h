@@ -481,6 +481,19 @@ CSA_API csa_status csa_set_batch_invariant(int on);
 CSA_API csa_status csa_selftest_bounded_wait(int sleeping, long long* out, cudaStream_t stream);
 
 /*
+ * csa_selftest_fp4_give_up -- csa_fp4_linear with one of its pipeline's barriers waiting for an
+ * arrival that never comes, so that the roles behind it give up (after about 0.1 s, here): the call
+ * ends like any other, y holds nothing of use, and csa_get_device_error reports CSA_DEVERR_TIMEOUT.
+ * barrier: 1 codes loaded, 2 stage free, 3 scales loaded, 4 scales in tensor memory, 5 tile done,
+ * 6 accumulator free, 7 partial sums received; ranks: bit r for CTA r of each cluster (1..255).
+ * Not every kernel waits on every barrier: a product that does not need the one named ends in
+ * time.  Supported: MXFP4 to bf16, NVFP4 to float32.  The pages have no counterpart: this is a test hook.
+ */
+CSA_API csa_status csa_selftest_fp4_give_up(int barrier, int ranks, csa_fp4_format fmt, int M, int N, int K, int G,
+                                            const csa_fp4_mat* x, const csa_fp4_mat* w, csa_dtype y_dtype, void* y,
+                                            int64_t ldy, cudaStream_t stream);
+
+/*
  * csa_mma_peak_probe -- dense tensor-core throughput probe (a measurement aid; the pages
  * have no counterpart).  `ctas` CTAs (one per SM) each issue `iters` rounds of four
  * tcgen05 MMAs of M = 128, N (16..256, a multiple of 16) and K = 64 block-scaled FP4

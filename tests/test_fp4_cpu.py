@@ -233,3 +233,15 @@ def test_rows_of_any_view_stay_in_its_storage(B, seed):
         assert rows * cols == t.numel() and (rows - 1) * ld + cols <= size
         assert torch.equal(base.as_strided((rows, cols), (ld, 1)), t.reshape(rows, cols))
     assert taken > 40
+
+
+def test_give_up_refusals(B):
+    L, P, I = B.lib(), ctypes.c_void_p, ctypes.c_int
+    f = L.csa_selftest_fp4_give_up
+    f.argtypes = [I, I, I, I, I, I, I, ctypes.POINTER(B._Fp4Mat), ctypes.POINTER(B._Fp4Mat), I, P, ctypes.c_int64, P]
+    for barrier, ranks in ((0, 1), (8, 1), (1, 0), (1, 256), (-1, 1)):
+        assert f(barrier, ranks, MX, 4, 256, 256, 1, mat(B), mat(B), BF16, P(16), 256, None) == INVALID
+    assert f(1, 1, MX, 4, 256, 256, 1, mat(B), mat(B), F32, P(16), 256, None) == UNSUPPORTED
+    assert f(1, 1, NV, 4, 256, 256, 1, mat(B, g=16), mat(B, g=16), BF16, P(16), 256, None) == UNSUPPORTED
+    assert f(1, 1, MX, 4, 256, 48, 1, mat(B), mat(B), BF16, P(16), 256, None) == UNSUPPORTED
+    assert f(1, 1, MX, 0, 256, 256, 1, mat(B), mat(B), BF16, None, 256, None) == 0
