@@ -544,3 +544,36 @@ def test_projection_of_zeros(B, cuda, T, H, D, G, Rk, d):
     assert not B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=one, z_scale=zero).any()
     assert not B.csa_grouped_out_proj_fp4(o, A, Bm, groups=G, o_scale=zero, z_scale=one).any()
     assert B.csa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_allocate_nothing(B, cuda, fmt):
+    """With out, workspace and the library's first calls behind them, the calls take no device memory, torch's
+    or their own."""
+    rng = np.random.default_rng(12)
+    A, _ = make(B, cuda, rng, 512, 256, fmt)
+    Bm, _ = make(B, cuda, rng, 1000, 512, fmt)
+    g = torch.tensor([6.0 / 2688], device=cuda) if fmt == "nvfp4" else None
+    sets = []
+    for T in (1, 40, 2000):
+        o = torch.randn((T, 8, 64), device=cuda).to(torch.bfloat16)
+        q = B.csa_fp4_quantize(o.reshape(T, 512), fmt=fmt, tensor_scale=g)
+        ws = torch.empty(B.csa_grouped_out_proj_fp4_workspace(fmt, T, 8, 64, 2, 256), dtype=torch.uint8, device=cuda)
+        new = lambda c, d=torch.bfloat16: torch.empty((T, c), dtype=d, device=cuda)  # noqa: E731,B023
+        sets.append((o, q, ws, new(512), new(512), new(512, torch.float32), new(1000)))
+
+    def run():
+        for o, q, ws, v, z, zf, y in sets:
+            B.csa_fp4_quantize(o.reshape(o.shape[0], 512), fmt=fmt, tensor_scale=g, out=q)
+            B.csa_fp4_dequantize(q, out=v)
+            B.csa_fp4_linear(q, A, groups=2, out=z)
+            B.csa_fp4_linear(q, A, groups=2, out=zf)
+            B.csa_grouped_out_proj_fp4(o, A, Bm, groups=2, o_scale=g, z_scale=g, out=y, workspace=ws)
+        torch.cuda.synchronize()
+
+    run()
+    free, held = torch.cuda.mem_get_info(cuda)[0], torch.cuda.memory_stats(cuda)["allocation.all.allocated"]
+    for _ in range(5):
+        run()
+    assert torch.cuda.memory_stats(cuda)["allocation.all.allocated"] == held
+    assert torch.cuda.mem_get_info(cuda)[0] == free
