@@ -25,9 +25,11 @@
 // tiles, 139 with pairs, 98 with the scales and the MMA issue as described here).  The 256
 // accumulator columns leave no room for a second accumulator next to the scales: the result warps
 // first read the tile into registers, release it, and convert and store while the next tile's MMAs
-// run.  A slab then takes 0.38 us: 87 GB/s per SM from L2, 0.27 us of MMAs.  Back to back for
-// seconds the power limit holds the clock near 1.6 GHz and the same product takes 115 us.  Pairs
-// of 384 tokens (44 KB for 1.5 times the work) measured the same.
+// run.  A slab then takes 0.38 us, of which 0.27 are MMAs, and the hand-over between two tiles
+// 1.5 us without MMAs (7 rounds: 10 of the 98 us).  An SM takes 35 KB a slab, 92 GB/s from L2, but
+// that is not what bounds it alone: pairs of 384 tokens (44 KB for 1.5 times the work) measured the
+// same, and neither L2 (34 % busy) nor the tensor pipe (56 %) is full.  Back to back for seconds the
+// power limit holds the clock near 1.6 GHz and the same product takes 115 us.
 //
 // Lone CTAs (kBN <= 128): with few tiles the K axis is split over the S CTAs of a cluster.  Each
 // CTA sends every other its float32 partial sums of that CTA's tokens (asynchronous stores into
@@ -859,7 +861,8 @@ cudaError_t launch_tile(const Fp4LinearArgs& a, LinearParams& p, int splits, cud
 //   set-up that no launch before it hides; twice the 30 and 1500 on a shared SM);
 //   unsplit results 10 a token.
 // In batch-invariant mode K is never split, so a row's sums run over K in one order whatever the
-// number of rows.
+// number of rows; few rows pay for it (x 4096 x 8192 MXFP4: 1 token 14.4 us for 6.5, 32 tokens 14.9
+// for 7.1, 128 tokens 15.3 for 11.1, 512 the same).
 struct Choice {
   int tokens, splits;
 };

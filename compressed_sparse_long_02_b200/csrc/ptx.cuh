@@ -479,9 +479,10 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {
 }
 
 // ------------------------------------------------------------------ programmatic dependent launch
-// Every kernel of this library waits for the grid it depends on before its first global
-// memory access, and lets its own dependents launch right away; the dependents then sit
-// in the same wait, so only the launch latency overlaps (no data is touched early).
+// Every kernel of this library waits for the grid it depends on before it reads or writes
+// global memory, and lets its own dependents launch right away; the dependents then sit in
+// the same wait, so the launch latency overlaps, and in the FP4 product a hint that asks for
+// its weights in L2 (a prefetch, whose result is never read from registers or shared memory).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void griddep_enter() {
