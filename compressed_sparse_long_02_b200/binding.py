@@ -510,7 +510,8 @@ def csa_fp4_scale_bytes(fmt: str, rows: int, cols: int) -> int:
 def csa_fp4_quantize(x: torch.Tensor, *, fmt: str = "mxfp4", tensor_scale: torch.Tensor | None = None,
                      out: Fp4Matrix | None = None) -> Fp4Matrix:
     """x [..., cols] float32/bf16 (evenly spaced rows, cols a multiple of 32) -> Fp4Matrix [rows, cols].
-    nvfp4 takes the tensor's scale (float32 [1], e.g. amax / 2688; 0 for a tensor of zeros); `out` reuses a matrix's buffers."""
+    nvfp4 takes the tensor's scale (float32 [1], e.g. amax / 2688, which is 0 for a tensor of zeros);
+    `out` reuses a matrix's buffers."""
     f, dt, dev = _fmt(fmt), _dt(x), x.device
     rows, cols, ld = _rows_2d(x, "x")
     if cols < 32 or cols % 32:

@@ -383,9 +383,9 @@ CSA_API csa_status csa_grouped_out_proj(int T, int H, int D, int G, int R, int d
  *                 NULL (MXFP4: g = 1).
  *
  * CSA_MXFP4: blocks of 32, the codes and UE8M0 scales of csa_quantize_mxfp4; value = code * 2^E.
- * CSA_NVFP4: blocks of 16, E4M3 scales (bytes 0..127, sign bit clear); value = code * s * g.  Encoding, every step rounded once
- *   to float32: s = e4m3(amax / (6 g)) (to nearest even, at most 448), T = s g,
- *   code = e2m1(x / T) (to nearest even, at most 6; 0 when T = 0); s = 0 in a block of zeros.
+ * CSA_NVFP4: blocks of 16, E4M3 scales (bytes 0..127, sign bit clear); value = code * s * g.
+ *   Encoding, every step rounded once to float32: s = e4m3(amax / (6 g)) (to nearest even, at most
+ *   448; 0 in a block of zeros), T = s g, code = e2m1(x / T) (to nearest even, at most 6; 0 when T = 0).
  * In both a NaN is left out of amax and encoded as +6 (0 when T = 0), and an infinity counts as
  * 2^128 in amax (E = 126; s = 448) and is encoded as +-6.
  *
